@@ -1,10 +1,12 @@
 /*
- * kvq.h -- C ABI of the B200 (sm_100a) per-token KV-cache epilogue library.
+ * kvq.h -- C ABI of the B200 (sm_100a) per-token KV-cache epilogue library,
+ * and of the attention and page operations that use its caches.
  *
  * One call per operation.  Each call validates its arguments on the host and,
- * if they are valid, enqueues exactly one kernel on the given CUDA stream and
- * returns.  Nothing is allocated, nothing is synchronised, no workspace is
- * needed; the caller owns every buffer.  Caches (and cache_scale) are updated
+ * if they are valid, enqueues its kernel (one, where nothing else is said) on
+ * the given CUDA stream and returns.  Nothing is allocated, nothing is
+ * synchronised, no workspace is needed except where a call names one; the
+ * caller owns every buffer.  Caches (and cache_scale) are updated
  * IN PLACE: only the rows addressed by a valid slot are written, and within a
  * row only the bytes the operation defines; every other byte keeps its value.
  * Execution is deterministic: each row has exactly one writer and no atomics
@@ -95,6 +97,7 @@ typedef enum {
 /* Fault bits of the device fault word. */
 #define KVQ_FAULT_SLOT_RANGE 0x1u   /* a slot/index outside [0, num_slots) and not -1 */
 #define KVQ_FAULT_TIMEOUT 0x2u      /* a pipeline wait gave up (an internal error; the output is incomplete) */
+#define KVQ_FAULT_NO_PAGE 0x4u      /* fork_pages found no free page for a child */
 
 /* ------------------------------------------------------------------------ */
 /* kv_compress_epilog                                                        */
@@ -299,6 +302,128 @@ KVQ_API kvq_status kvq_dequant_rope_quant_kvcache(const kvq_tensor* x, const kvq
 /* ------------------------------------------------------------------------ */
 KVQ_API kvq_status kvq_compressor(const kvq_tensor* x, const kvq_tensor* w_kv, const kvq_tensor* w_gate,
                                   const kvq_tensor* ape, kvq_tensor* cmp_kv, int32_t cmp_ratio, kvq_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* prompt_attention: causal attention over whole prompts, grouped heads,     */
+/* packed sequences of different lengths.  Reads what                        */
+/* dequant_rope_quant_kvcache leaves in q_out, k_out and v_out.              */
+/*                                                                           */
+/* q, out   bf16 or f16 [T, Nq, D] (packed, with cu_seqlens_q) or             */
+/*          [B, S, Nq, D]; k, v the same type, [Tk, Nkv, D] or                */
+/*          [B, Sk, Nkv, D].  D = 64 or 128, Nq a multiple of Nkv (at most    */
+/*          128 times); query head h reads key head h / (Nq / Nkv).  D        */
+/*          contiguous, token and head strides multiples of 8 elements, data  */
+/*          16-byte aligned (slices of one fused projection are fine).        */
+/* cu_seqlens_q, cu_seqlens_k   int32 [B + 1], contiguous: sequence b holds   */
+/*          the rows [cu[b], cu[b + 1]).  cu_seqlens_k NULL: as the queries.  */
+/*          Both NULL for the 4-D form.  Rows of out that no sequence holds   */
+/*          keep their contents; a span outside the tensor counts as an empty */
+/*          sequence and sets KVQ_FAULT_SLOT_RANGE.                            */
+/* causal   nonzero: query i of a sequence with lq queries and lk keys sees   */
+/*          the keys j <= i + lk - lq (its own token is the last one it sees, */
+/*          also behind a cached context); 0: every key of the sequence.      */
+/* lse      NULL or f32 [T, Nq] ([B, S, Nq]), contiguous: log of the sum of   */
+/*          exp(score), for merging with other keys.                          */
+/* Per row: out = sum_j softmax_j(softmax_scale * q . k_j) v_j.  A row that   */
+/* sees no key: out 0, lse -inf.  Scores, maxima, sums and the output         */
+/* accumulate in fp32; the weights are rounded to q's type for the product    */
+/* with v.  One kernel on `stream`; nothing is allocated; no workspace.       */
+/* ------------------------------------------------------------------------ */
+KVQ_API kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k, const kvq_tensor* v,
+                                        const kvq_tensor* cu_seqlens_q, const kvq_tensor* cu_seqlens_k,
+                                        kvq_tensor* out, kvq_tensor* lse, int32_t causal, float softmax_scale,
+                                        kvq_stream stream);
+
+/* ------------------------------------------------------------------------ */
+/* shared_prefix_attention: one new token per request over a paged cache,    */
+/* for a batch whose requests share a prefix; the prefix is read once for    */
+/* all requests.  Reads the caches that dequant_rope_quant_kvcache writes in */
+/* page mode (int8), or 16-bit caches of the same shape.                      */
+/*                                                                           */
+/* q, out   bf16 or f16 [B, Nq, D]; D = 64 or 128, strides as above.          */
+/* k_cache, v_cache   [num_pages, block, Nkv, D], int8 or q's type; only the  */
+/*          page dimension strided (a multiple of 16 bytes), 16-byte aligned. */
+/* scale_k, scale_v   f32, Nkv*D elements, required for int8 caches:          */
+/* offset_k, offset_v value = (code - offset) * scale; offsets optional.      */
+/*          NULL (else KVQ_ERR_ATTR) for 16-bit caches.                        */
+/* block_table   int32 [B, cols], columns contiguous, any row stride (0 too): */
+/*          the pages of each request's own tokens, which follow the prefix.  */
+/* seq_lens int32 [B]: own tokens of each request, 0 .. cols * block; -1: the */
+/*          row takes no part and its out and lse keep their contents.        */
+/* prefix_table  int32, at least ceil(prefix_len / block) pages (NULL when    */
+/*          prefix_len is 0); the last page may be partly filled.             */
+/* A page number outside the cache drops that page's tokens, and a length     */
+/* that does not fit drops the row; both set KVQ_FAULT_SLOT_RANGE.             */
+/* lse      NULL or f32 [B, Nq].  A row without keys: out 0, lse -inf.         */
+/* workspace  uint8, kvq_shared_prefix_attention_workspace() bytes (NULL if   */
+/*          0), 16-byte aligned; its contents need no initialisation and mean */
+/*          nothing afterwards.  Calls that may run at the same time need one */
+/*          each.                                                              */
+/* Arithmetic as prompt_attention's; int8 codes enter the products exactly    */
+/* and the scales in fp32.                                                     */
+/* ------------------------------------------------------------------------ */
+KVQ_API kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_cache,
+                                               const kvq_tensor* v_cache, const kvq_tensor* block_table,
+                                               const kvq_tensor* seq_lens, const kvq_tensor* prefix_table,
+                                               int64_t prefix_len, const kvq_tensor* scale_k,
+                                               const kvq_tensor* scale_v, const kvq_tensor* offset_k,
+                                               const kvq_tensor* offset_v, kvq_tensor* out, kvq_tensor* lse,
+                                               float softmax_scale, kvq_tensor* workspace, kvq_stream stream);
+
+/* Bytes of workspace of a call with these sizes (max_own: cols * block of the
+ * block table), or -1 for sizes the call refuses. */
+KVQ_API int64_t kvq_shared_prefix_attention_workspace(int64_t batch, int64_t n_q, int64_t n_kv, int64_t dim,
+                                                      int64_t prefix_len, int64_t max_own);
+
+/* ------------------------------------------------------------------------ */
+/* Pages of a cache.  Page i is element i of the first dimension of every    */
+/* cache; `caches` are up to 64 tensors [num_pages, ...] of any types (keys,  */
+/* values, scales, several layers), each page contiguous and at most 2^31-1   */
+/* bytes, only the page dimension strided.  They must not overlap.            */
+/* ref_count   int32 [num_pages], contiguous: the table rows that hold a      */
+/*             page; 0: free.                                                  */
+/* block_table int32 [rows, cols], columns contiguous: a row's pages in token */
+/*             order, -1 behind them.  seq_lens int32 [rows]: its tokens.      */
+/* Page, row and index values are int32, or int64 where an index tensor is    */
+/* (src, dst, rows, parents, children).                                        */
+/* ------------------------------------------------------------------------ */
+
+/* copy_pages: in every cache, page dst[i] = page src[i], i = 0 .. n-1; a -1 on
+ * either side skips the pair, other values outside the cache skip it and set
+ * KVQ_FAULT_SLOT_RANGE.  No page may be both a source and a destination of
+ * one call, nor twice a destination (not detected; undefined contents). */
+KVQ_API kvq_status kvq_copy_pages(const kvq_tensor* caches, int32_t n_caches, const kvq_tensor* src,
+                                  const kvq_tensor* dst, kvq_stream stream);
+
+/* free_pages: each named row gives up its pages (ref_count - 1), its entries
+ * become -1 and its length 0.  Empty rows, rows named twice and -1 are no-ops
+ * the second time; rows, pages or lengths out of range, and pages that are
+ * free already, are skipped and set KVQ_FAULT_SLOT_RANGE. */
+KVQ_API kvq_status kvq_free_pages(kvq_tensor* block_table, kvq_tensor* seq_lens, kvq_tensor* ref_count,
+                                  const kvq_tensor* rows, int64_t block_size, kvq_stream stream);
+
+/* fork_pages: row children[i], which must be empty, becomes a copy of row
+ * parents[i]: it shares the parent's full pages (ref_count + 1) and gets a
+ * page of its own, with the parent's contents in every cache, for the last
+ * one if it is partly filled.  The lowest free pages are taken, in the order
+ * of the children.  fresh (int32 [n]) receives that page, -1 if there was
+ * nothing to copy, or -2 for a child that is left empty: no page was free
+ * (KVQ_FAULT_NO_PAGE), or a row or length out of range, a child that is not
+ * empty, named before or itself a parent (KVQ_FAULT_SLOT_RANGE).  A pair
+ * (-1, -1) is skipped.  Two kernels on `stream`. */
+KVQ_API kvq_status kvq_fork_pages(const kvq_tensor* caches, int32_t n_caches, kvq_tensor* block_table,
+                                  kvq_tensor* seq_lens, kvq_tensor* ref_count, const kvq_tensor* parents,
+                                  const kvq_tensor* children, int64_t block_size, kvq_tensor* fresh,
+                                  kvq_stream stream);
+
+/* compact_pages: the U pages in use move to the numbers 0 .. U-1: those below
+ * U stay, the others take the free ones below U, both in ascending order.
+ * page_map (int32 [num_pages]) receives each page's new number (-1: free);
+ * new_table and new_ref_count the renumbered table and counts (either may be
+ * the old one; else the old one is left as it is).  Two kernels on `stream`. */
+KVQ_API kvq_status kvq_compact_pages(const kvq_tensor* caches, int32_t n_caches, const kvq_tensor* block_table,
+                                     const kvq_tensor* ref_count, kvq_tensor* new_table, kvq_tensor* new_ref_count,
+                                     kvq_tensor* page_map, kvq_stream stream);
 
 /* ------------------------------------------------------------------------ */
 /* Utilities                                                                 */

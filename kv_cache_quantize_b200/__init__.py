@@ -1,4 +1,5 @@
-"""B200-native per-token KV-cache epilogue: Python binding of libkvq.so.
+"""B200-native per-token KV-cache epilogue, and the attention and page operations
+on its caches: Python binding of libkvq.so.
 
 Thin ctypes marshalling over the C ABI in include/kvq.h -- every step of the
 epilogue runs in the library's sm_100a kernels; torch supplies device memory
@@ -8,6 +9,9 @@ first call raises.
 Operations (same names as the C ABI without the ``kvq_`` prefix):
   kv_compress_epilog, indexer_quant_cache, kv_rmsnorm_rope_cache,
   dequant_rope_quant_kvcache; the packed-row decoder kv_decompress;
+  the attention over prompts, prompt_attention, and over a paged cache,
+  shared_prefix_attention; the pages of a cache: copy_pages, free_pages,
+  fork_pages, compact_pages;
   utilities get_error, kv_cache_col, indexer_scale_col, convert.
 
 Device faults.  A call returns once its kernel is enqueued; a slot outside
@@ -21,6 +25,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
+import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -29,7 +34,9 @@ __all__ = [
     "KvqError", "KvqFault", "lib", "library_path", "kv_compress_epilog", "kv_decompress", "indexer_quant_cache",
     "kv_rmsnorm_rope_cache",
     "dequant_rope_quant_kvcache", "compressor", "get_error", "kv_cache_col", "indexer_scale_col", "convert", "selftest", "scatter_rows",
-    "FAULT_SLOT_RANGE", "FAULT_TIMEOUT", "STATUS",
+    "prompt_attention", "shared_prefix_attention", "shared_prefix_attention_workspace",
+    "copy_pages", "free_pages", "fork_pages", "compact_pages",
+    "FAULT_SLOT_RANGE", "FAULT_TIMEOUT", "FAULT_NO_PAGE", "STATUS",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -39,6 +46,7 @@ _LIB: Optional[ctypes.CDLL] = None
 MAX_DIMS = 8
 FAULT_SLOT_RANGE = 0x1
 FAULT_TIMEOUT = 0x2
+FAULT_NO_PAGE = 0x4
 STATUS = {0: "KVQ_OK", 1: "KVQ_ERR_NULL", 2: "KVQ_ERR_NDIM", 3: "KVQ_ERR_SHAPE", 4: "KVQ_ERR_DTYPE",
           5: "KVQ_ERR_ATTR", 6: "KVQ_ERR_LAYOUT", 7: "KVQ_ERR_CAPACITY", 8: "KVQ_ERR_CUDA",
           9: "KVQ_ERR_UNSUPPORTED"}
@@ -65,10 +73,11 @@ class KvqError(RuntimeError):
 
 
 class KvqFault(RuntimeError):
-    """Device fault bits (FAULT_SLOT_RANGE, FAULT_TIMEOUT) found after an operation run with check=True."""
+    """Device fault bits (FAULT_SLOT_RANGE, FAULT_TIMEOUT, FAULT_NO_PAGE) found after an operation run with check=True."""
     def __init__(self, op: str, bits: int):
         self.bits = bits
-        names = [n for b, n in ((FAULT_SLOT_RANGE, "FAULT_SLOT_RANGE"), (FAULT_TIMEOUT, "FAULT_TIMEOUT")) if bits & b]
+        names = [n for b, n in ((FAULT_SLOT_RANGE, "FAULT_SLOT_RANGE"), (FAULT_TIMEOUT, "FAULT_TIMEOUT"),
+                             (FAULT_NO_PAGE, "FAULT_NO_PAGE")) if bits & b]
         super().__init__(f"{op}: device fault bits {bits:#x} ({', '.join(names) or 'unknown'})")
 
 
@@ -93,6 +102,14 @@ def lib() -> ctypes.CDLL:
         L.kvq_get_error.argtypes = [vp, ctypes.POINTER(ctypes.c_uint32)]
         L.kvq_scatter_rows.argtypes = [_P, _P, _P, i64, vp]
         L.kvq_compressor.argtypes = [_P, _P, _P, _P, _P, i32, vp]
+        L.kvq_prompt_attention.argtypes = [vp] * 7 + [i32, ctypes.c_float, vp]
+        L.kvq_shared_prefix_attention.argtypes = [vp] * 6 + [i64] + [vp] * 6 + [ctypes.c_float, vp, vp]
+        L.kvq_shared_prefix_attention_workspace.argtypes = [i64] * 6
+        L.kvq_shared_prefix_attention_workspace.restype = i64
+        L.kvq_copy_pages.argtypes = [vp, i32, vp, vp, vp]
+        L.kvq_free_pages.argtypes = [vp, vp, vp, vp, i64, vp]
+        L.kvq_fork_pages.argtypes = [vp, i32, vp, vp, vp, vp, vp, i64, vp, vp]
+        L.kvq_compact_pages.argtypes = [vp, i32, vp, vp, vp, vp, vp, vp]
         L.kvq_convert.argtypes = [i32, vp, i64, vp, vp]
         L.kvq_selftest.argtypes = [i32, ctypes.POINTER(ctypes.c_uint64), vp]
         L.kvq_kv_cache_col.argtypes = [i64, i32, i32]
@@ -105,7 +122,8 @@ def lib() -> ctypes.CDLL:
         for name in ("kvq_kv_compress_epilog", "kvq_kv_decompress", "kvq_indexer_quant_cache",
                      "kvq_kv_rmsnorm_rope_cache",
                      "kvq_dequant_rope_quant_kvcache", "kvq_get_error", "kvq_convert", "kvq_selftest",
-                     "kvq_scatter_rows", "kvq_compressor"):
+                     "kvq_scatter_rows", "kvq_compressor", "kvq_prompt_attention", "kvq_shared_prefix_attention",
+                     "kvq_copy_pages", "kvq_free_pages", "kvq_fork_pages", "kvq_compact_pages"):
             getattr(L, name).restype = i32
         _LIB = L
     return _LIB
@@ -324,8 +342,194 @@ def scatter_rows(x: torch.Tensor, slot_mapping: torch.Tensor, cache: torch.Tenso
 
 
 # ---------------------------------------------------------------------------
+# Attention and page operations.  These run once per layer and step, where a
+# few microseconds on the host count: their descriptors are packed into one
+# buffer with struct instead of one ctypes object each.
+_DESC = [struct.Struct("@Pii" + f"{n}q{8 * (MAX_DIMS - n)}x" + f"{n}q{8 * (MAX_DIMS - n)}x")
+         for n in range(MAX_DIMS + 1)]
+_DESC_BYTES = ctypes.sizeof(KvqTensor)
+
+
+def _pack(op: str, tensors, device: Optional[torch.device]):
+    """Descriptors of the tensors (None allowed) side by side: the buffer, their
+    addresses (None for None), and their one CUDA device."""
+    buf = bytearray(_DESC_BYTES * len(tensors))
+    base = ctypes.addressof((ctypes.c_char * len(buf)).from_buffer(buf)) if tensors else 0
+    at = []
+    off = 0
+    for t in tensors:
+        if t is None:
+            at.append(None)
+            continue
+        if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor):
+            raise TypeError(f"{op}: expected a tensor, got {type(t).__name__}")
+        code = _DTYPES.get(t.dtype)
+        if code is None:
+            raise TypeError(f"dtype {t.dtype} has no kvq equivalent")
+        shape = t.shape
+        n = len(shape)
+        if n > MAX_DIMS:
+            raise ValueError("too many dimensions")
+        ptr = t.data_ptr()
+        if 0 in shape:
+            ptr = 0
+        else:
+            dev = t.device
+            if dev != device:
+                if dev.type != "cuda":
+                    raise ValueError(f"{op}: tensors must be on a CUDA device, got one on {dev}")
+                if device is not None:
+                    raise ValueError(f"{op}: tensors on {device} and {dev}; all must be on one device")
+                device = dev
+        _DESC[n].pack_into(buf, off, ptr, code, n, *shape, *t.stride())
+        at.append(base + off)
+        off += _DESC_BYTES
+    return buf, at, device
+
+
+def _run(op: str, call, stream, check: bool, dev: Optional[torch.device]) -> None:
+    """Call the library with the device current and the stream chosen as for every operation."""
+    with _on(dev):
+        if stream is None:
+            st = torch.cuda.current_stream(dev).cuda_stream if dev is not None else 0
+        else:
+            st = _stream(stream)
+        _check(op, call(st))
+        _faults(op, check, st)
+
+
+def _using(stream, device):
+    """Allocate on the call's own stream, so that the memory is not handed on before the call has used it."""
+    if stream is None:
+        return contextlib.nullcontext()
+    if not isinstance(stream, torch.cuda.Stream):
+        stream = torch.cuda.ExternalStream(int(stream), device=device)
+    return torch.cuda.stream(stream)
+
+
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
+    """An output or workspace of a call on `stream` (None: the current one)."""
+    if stream is None or device.type != "cuda":
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.device(device), _using(stream, device):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
+def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor] = None,
+                     cu_seqlens_k: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, causal: bool = True, softmax_scale: Optional[float] = None,
+                     stream=None, check: bool = False) -> torch.Tensor:
+    """Causal attention over whole prompts with grouped heads (see kvq_prompt_attention): q [T, Nq, D] with
+    cu_seqlens_q [B + 1] (packed sequences of different lengths), or q [B, S, Nq, D]; k and v with Nkv heads,
+    cu_seqlens_k where a sequence has other keys than queries (a cached context in front).  Returns out, like q;
+    rows that no sequence holds are not written.  softmax_scale defaults to D ** -0.5.  Spans outside the tensors
+    are reported by get_error(), or raised here with check=True."""
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    if softmax_scale is None:
+        softmax_scale = q.shape[-1] ** -0.5 if q.dim() and q.shape[-1] else 1.0
+    buf, d, dev = _pack("prompt_attention", (q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse), None)
+    call = lib().kvq_prompt_attention
+    _run("prompt_attention", lambda st: call(*d, 1 if causal else 0, softmax_scale, st), stream, check, dev)
+    return out
+
+
+def shared_prefix_attention_workspace(batch: int, n_q: int, n_kv: int, dim: int, prefix_len: int,
+                                      max_own: int) -> int:
+    """Bytes of workspace of a shared_prefix_attention call (max_own: block_table's columns x tokens per page);
+    -1 for sizes that it refuses."""
+    return int(lib().kvq_shared_prefix_attention_workspace(batch, n_q, n_kv, dim, prefix_len, max_own))
+
+
+def shared_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                            seq_lens: torch.Tensor, prefix_table: Optional[torch.Tensor] = None, prefix_len: int = 0,
+                            scale_k: Optional[torch.Tensor] = None, scale_v: Optional[torch.Tensor] = None,
+                            offset_k: Optional[torch.Tensor] = None, offset_v: Optional[torch.Tensor] = None,
+                            out: Optional[torch.Tensor] = None, lse: Optional[torch.Tensor] = None,
+                            softmax_scale: Optional[float] = None, workspace: Optional[torch.Tensor] = None,
+                            stream=None, check: bool = False) -> torch.Tensor:
+    """Attention of one new token per request over a paged cache (see kvq_shared_prefix_attention): the first
+    prefix_len keys, in the pages of prefix_table, are shared by all requests and read once; request b's own
+    seq_lens[b] keys follow in the pages block_table[b].  int8 caches need scale_k and scale_v.  Returns out, like
+    q [B, Nq, D]; rows with seq_lens -1 are not written.  The workspace is allocated when not given (uint8,
+    shared_prefix_attention_workspace() bytes, one per call that may run at the same time).  Bad pages and lengths
+    are reported by get_error(), or raised here with check=True."""
+    if out is None:
+        out = _empty(q.shape, q.dtype, q.device, stream)
+    if softmax_scale is None:
+        softmax_scale = q.shape[-1] ** -0.5 if q.dim() and q.shape[-1] else 1.0
+    L = lib()
+    prefix_len = int(prefix_len)
+    if workspace is None and q.dim() == 3 and k_cache.dim() == 4 and block_table.dim() == 2:
+        need = L.kvq_shared_prefix_attention_workspace(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], prefix_len,
+                                                       block_table.shape[1] * k_cache.shape[1])
+        if need > 0:
+            workspace = _empty((need,), torch.uint8, q.device, stream)
+    buf, d, dev = _pack("shared_prefix_attention", (q, k_cache, v_cache, block_table, seq_lens, prefix_table, scale_k,
+                                                    scale_v, offset_k, offset_v, out, lse, workspace), None)
+    call = L.kvq_shared_prefix_attention
+    _run("shared_prefix_attention", lambda st: call(*d[:6], prefix_len, *d[6:12], softmax_scale, d[12], st), stream,
+         check, dev)
+    return out
+
+
+def copy_pages(caches: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.Tensor, stream=None,
+               check: bool = False) -> None:
+    """In every cache [num_pages, ...], page dst[i] = page src[i] (see kvq_copy_pages); pairs with a -1 are
+    skipped.  Pages out of range are reported by get_error(), or raised here with check=True."""
+    caches = list(caches)
+    buf, d, dev = _pack("copy_pages", (*caches, src, dst), None)
+    call = lib().kvq_copy_pages
+    _run("copy_pages", lambda st: call(d[0], len(caches), d[-2], d[-1], st), stream, check, dev)
+
+
+def free_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_count: torch.Tensor, rows: torch.Tensor,
+               block_size: int, stream=None, check: bool = False) -> None:
+    """Give up the pages of the named rows (see kvq_free_pages): counts down by one, entries -1, lengths 0."""
+    buf, d, dev = _pack("free_pages", (block_table, seq_lens, ref_count, rows), None)
+    call = lib().kvq_free_pages
+    _run("free_pages", lambda st: call(*d, int(block_size), st), stream, check, dev)
+
+
+def fork_pages(caches: Sequence[torch.Tensor], block_table: torch.Tensor, seq_lens: torch.Tensor,
+               ref_count: torch.Tensor, parents: torch.Tensor, children: torch.Tensor, block_size: int,
+               fresh: Optional[torch.Tensor] = None, stream=None, check: bool = False) -> torch.Tensor:
+    """Make the empty rows `children` copies of the rows `parents` (see kvq_fork_pages): full pages are shared, a
+    partly filled last page is copied into the lowest free page.  Returns fresh, int32: that page for each child,
+    -1 where nothing had to be copied, -2 for a child left empty (bits FAULT_NO_PAGE or FAULT_SLOT_RANGE, reported
+    by get_error(), or raised here with check=True)."""
+    caches = list(caches)
+    if fresh is None:
+        fresh = _empty(children.shape, torch.int32, children.device, stream)
+    buf, d, dev = _pack("fork_pages", (*caches, block_table, seq_lens, ref_count, parents, children, fresh), None)
+    call = lib().kvq_fork_pages
+    _run("fork_pages", lambda st: call(d[0], len(caches), *d[-6:-1], int(block_size), d[-1], st), stream, check, dev)
+    return fresh
+
+
+def compact_pages(caches: Sequence[torch.Tensor], block_table: torch.Tensor, ref_count: torch.Tensor,
+                  new_table: Optional[torch.Tensor] = None, new_ref_count: Optional[torch.Tensor] = None,
+                  page_map: Optional[torch.Tensor] = None, stream=None,
+                  check: bool = False) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+    """Move the pages in use to the lowest page numbers, in every cache (see kvq_compact_pages).  Returns
+    (new_table, new_ref_count, page_map), allocated when not given; new_table and new_ref_count may be the old
+    ones, else those are left as they are."""
+    caches = list(caches)
+    if new_table is None:
+        new_table = _empty(block_table.shape, torch.int32, block_table.device, stream)
+    if new_ref_count is None:
+        new_ref_count = _empty(ref_count.shape, torch.int32, ref_count.device, stream)
+    if page_map is None:
+        page_map = _empty(ref_count.shape, torch.int32, ref_count.device, stream)
+    buf, d, dev = _pack("compact_pages", (*caches, block_table, ref_count, new_table, new_ref_count, page_map), None)
+    call = lib().kvq_compact_pages
+    _run("compact_pages", lambda st: call(d[0], len(caches), *d[-5:], st), stream, check, dev)
+    return new_table, new_ref_count, page_map
+
+
+# ---------------------------------------------------------------------------
 def get_error(stream=None, device=None) -> int:
-    """Wait for the stream, return and clear the fault bits (FAULT_SLOT_RANGE, FAULT_TIMEOUT) of the
+    """Wait for the stream, return and clear the fault bits (FAULT_SLOT_RANGE, FAULT_TIMEOUT, FAULT_NO_PAGE) of the
     device in one atomic read-and-clear on the device.  The device is `device`, else the
     stream's, else the current one."""
     if device is None and isinstance(stream, torch.cuda.Stream):

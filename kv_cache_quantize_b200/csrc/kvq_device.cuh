@@ -19,9 +19,9 @@ constexpr unsigned FULL_MASK = 0xffffffffu;
 
 // ---------------------------------------------------------------------------
 // Device fault word: data faults (a bad slot) set bits here; the host reads
-// and clears it with kvq_get_error.  One word per device (module global).
+// and clears it with kvq_get_error.  One word per device and translation unit.
 // ---------------------------------------------------------------------------
-__device__ unsigned int g_fault_word;
+static __device__ unsigned int g_fault_word;
 constexpr unsigned FAULT_SLOT_RANGE = 0x1u;
 
 __device__ __forceinline__ void raise_fault(unsigned bits) { atomicOr(&g_fault_word, bits); }
