@@ -2,6 +2,7 @@
 // prompt_attention and shared_prefix_attention.
 #include "kvq_host.cuh"
 #include "attention_common.cuh"
+#include "attention_prompt.cuh"
 #include "attention_simple.cuh"
 
 namespace kvq {
@@ -15,6 +16,7 @@ namespace {
 
 // tokens of one tensor and rows of one launch: 32-bit row numbers with room for a tile
 constexpr int64_t ATT_MAX_TOKENS = 0x40000000;
+constexpr int64_t ATT_MAX_STRIDE = int64_t(1) << 38;      // elements: a tensor map holds 40-bit byte strides
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
@@ -36,7 +38,8 @@ kvq_status attn_rows(const kvq_tensor* t, int64_t* tokens, int64_t* heads, int64
         else if (t->shape[0] > 1 && t->stride[0] != t->shape[1] * t->stride[1]) return KVQ_ERR_LAYOUT;
     }
     if (*tokens == 1) r->tok = *heads * *dim;
-    if (r->head < 0 || r->tok < 0 || r->head % 8 != 0 || r->tok % 8 != 0) return KVQ_ERR_LAYOUT;
+    if (r->head % 8 != 0 || r->tok % 8 != 0) return KVQ_ERR_LAYOUT;
+    if (r->head < *dim || r->tok < *dim || r->head >= ATT_MAX_STRIDE || r->tok >= ATT_MAX_STRIDE) return KVQ_ERR_LAYOUT;
     return KVQ_OK;
 }
 
@@ -49,6 +52,39 @@ bool disjoint_rows(const AttnRows& r, int64_t tokens, int64_t heads, int64_t dim
 }
 
 int att_type(int32_t dt) { return dt == KVQ_BF16 ? ATT_BF16 : (dt == KVQ_F16 ? ATT_F16 : (dt == KVQ_I8 ? ATT_I8 : -1)); }
+
+// [tokens, heads, D] rows of a 16-bit type in boxes of box_tok x box_heads x 64
+// values with the 128-byte swizzle; tokens past the end read as zero.
+bool rows_map(CUtensorMap* m, int type, const AttnRows& r, int64_t tokens, int64_t heads, int64_t D, int box_heads,
+              int box_tok) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)tokens};
+    const cuuint64_t strides[2] = {(cuuint64_t)(r.head * 2), (cuuint64_t)(r.tok * 2)};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_heads, (cuuint32_t)box_tok};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    return enc(m, type == ATT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3, r.base, dims,
+               strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int T, int D>
+kvq_status run_prompt(const PromptArgs& a, cudaStream_t s) {
+    const int tok = 128 / a.G;
+    CUtensorMap mq, mk, mv;
+    // without keys nothing is loaded; the maps still need memory to point at
+    const AttnRows& k = a.Tk > 0 ? a.k : a.q;
+    const AttnRows& v = a.Tk > 0 ? a.v : a.q;
+    const int64_t tk = a.Tk > 0 ? a.Tk : a.T, nkv = a.Tk > 0 ? a.Nkv : a.Nq;
+    if (!rows_map(&mq, T, a.q, a.T, a.Nq, D, a.G, tok) || !rows_map(&mk, T, k, tk, nkv, D, 1, PA_KEYS) ||
+        !rows_map(&mv, T, v, tk, nkv, D, 1, PA_KEYS))
+        return KVQ_ERR_CUDA;
+    const int64_t items = (a.T / (2 * tok) + a.B) * a.Nkv;       // at least the number of work items
+    auto kernel = prompt_kernel<T, D>;
+    constexpr uint32_t smem = pa_smem_bytes(D);
+    return launched(launch(kernel, (unsigned)persistent_grid(kernel, PA_THREADS, items, smem), PA_THREADS, smem, s, mq, mk,
+                           mv, a));
+}
 
 }  // namespace
 
@@ -123,11 +159,8 @@ kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k, const 
     a.causal = causal != 0;
     a.scale = softmax_scale;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto go = [&](auto kernel) {
-        return launched(launch(kernel, (unsigned)persistent_grid(kernel, 128, (a.T * a.Nq + 3) / 4), 128, 0, s, a));
-    };
-    if (type == ATT_BF16) return D == 64 ? go(prompt_simple_kernel<ATT_BF16, 64>) : go(prompt_simple_kernel<ATT_BF16, 128>);
-    return D == 64 ? go(prompt_simple_kernel<ATT_F16, 64>) : go(prompt_simple_kernel<ATT_F16, 128>);
+    if (type == ATT_BF16) return D == 64 ? run_prompt<ATT_BF16, 64>(a, s) : run_prompt<ATT_BF16, 128>(a, s);
+    return D == 64 ? run_prompt<ATT_F16, 64>(a, s) : run_prompt<ATT_F16, 128>(a, s);
 }
 
 int64_t kvq_shared_prefix_attention_workspace(int64_t batch, int64_t n_q, int64_t n_kv, int64_t dim,

@@ -1,4 +1,4 @@
-// attention_simple.cuh -- the attention calls in their simplest form: one warp
+// attention_simple.cuh -- the paged attention in its simplest form: one warp
 // per query row, one key at a time, softmax by a running maximum and sum.
 #pragma once
 
@@ -25,47 +25,6 @@ struct RowState {
         m = mn;
     }
 };
-
-template <int T, int D>
-__global__ void __launch_bounds__(128) prompt_simple_kernel(const PromptArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    pdl_wait();
-    pdl_trigger();
-    const int64_t nw = ((int64_t)gridDim.x * blockDim.x) >> 5;
-    for (int64_t w = ((int64_t)blockIdx.x * blockDim.x + threadIdx.x) >> 5; w < a.T * a.Nq; w += nw) {
-        const int64_t t = w / a.Nq;
-        const int h = (int)(w - t * a.Nq);
-        int b = 0;
-        SeqSpan s;
-        for (; b < a.B; ++b) {
-            s = prompt_span(a, b, lane == 0);
-            if (t >= s.q0 && t < s.q0 + s.lq) break;
-        }
-        if (b == a.B) continue;                               // a row behind the last sequence
-        const int64_t i = t - s.q0;
-        const int64_t see = a.causal ? i + 1 + s.lk - s.lq : s.lk;
-        float q[E];
-#pragma unroll
-        for (int e = 0; e < E; ++e) q[e] = att_load<T>(a.q.base, t * a.q.tok + h * a.q.head + lane + 32 * e);
-        RowState r;
-        r.init();
-        for (int64_t j = 0; j < see; ++j) {
-            const int64_t ko = (s.k0 + j) * a.k.tok + (h / a.G) * a.k.head, vo = (s.k0 + j) * a.v.tok + (h / a.G) * a.v.head;
-            float d = 0.0f, v[E];
-#pragma unroll
-            for (int e = 0; e < E; ++e) {
-                d = __fmaf_rn(q[e], att_load<T>(a.k.base, ko + lane + 32 * e), d);
-                v[e] = att_load<T>(a.v.base, vo + lane + 32 * e);
-            }
-            r.key(warp_sum(d) * (a.scale * ATT_LOG2E), v);
-        }
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            att_store<T>(a.out.base, t * a.out.tok + h * a.out.head + lane + 32 * e, r.l > 0.0f ? __fdiv_rn(r.acc[e], r.l) : (see > 0 ? r.acc[e] + r.l : 0.0f));
-        if (a.lse && lane == 0) a.lse[t * a.Nq + h] = see > 0 ? (r.m + log2f(r.l)) * ATT_LN2 : -INFINITY;
-    }
-}
 
 template <int T, int C, int D>
 __global__ void __launch_bounds__(128) shared_simple_kernel(const SharedArgs a) {

@@ -64,7 +64,8 @@ def prompt(L, base=PROMPT, **kw):
     ({"out": t((50, 4, 128), BF)}, ESHAPE),
     ({"q": t((50, 129, 128), BF), "out": t((50, 129, 128), BF), "k": t((60, 1, 128), BF), "v": t((60, 1, 128), BF)}, EUNSUP),
     ({"q": t((50, 8, 128), BF, (2048, 256, 2))}, ELAYOUT), ({"q": t((50, 8, 128), BF, (1028, 128, 1))}, ELAYOUT),
-    ({"k": t((60, 2, 128), BF, (300, 132, 1))}, ELAYOUT), ({"out": t((50, 8, 128), BF, (0, 128, 1))}, ELAYOUT),
+    ({"k": t((60, 2, 128), BF, (300, 132, 1))}, ELAYOUT), ({"k": t((60, 2, 128), BF, (0, 128, 1))}, ELAYOUT),
+    ({"v": t((60, 2, 128), BF, (256, 0, 1))}, ELAYOUT), ({"q": t((50, 8, 128), BF, (1024, 120, 1))}, ELAYOUT), ({"out": t((50, 8, 128), BF, (0, 128, 1))}, ELAYOUT),
     ({"out": t((50, 8, 128), BF, (1024, 64, 1))}, ELAYOUT),
     ({"cu_q": t((4,), I64)}, EDTYPE), ({"cu_k": t((5,), I32)}, ESHAPE), ({"cu_q": t((1, 4), I32)}, ENDIM),
     ({"cu_q": t((0,), I32), "cu_k": t((0,), I32)}, ESHAPE), ({"cu_q": t((4,), I32, (2,))}, ELAYOUT),
@@ -222,7 +223,7 @@ def test_binding_refuses_host_tensors_and_other_types(L):
     with pytest.raises(TypeError):
         kvq.prompt_attention(q.double(), q, q, cu)
     with pytest.raises(TypeError):
-        kvq.free_pages(cu[None], cu, cu, [1, 2], 16)
+        kvq.free_pages([[1, 2]], cu, cu, cu, 16)
 
 
 def test_descriptors_of_the_packed_form_are_those_of_desc():

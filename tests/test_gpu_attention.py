@@ -122,9 +122,9 @@ def test_prompt_strides_and_unused_rows():
     ot = torch.full((8, t, 128), 3.0, dtype=BF, device="cuda").transpose(0, 1)
     kvq.prompt_attention(q, kt, vt, i32(cu(lens)), out=ot, check=True)
     assert torch.equal(ot[:sum(lens)], store[:sum(lens), :, :128]) and bool((ot[sum(lens):] == 3.0).all())
-    # one token's keys for all (stride 0)
-    one = k[:1].expand(t, 2, 128)
-    run_prompt(q, one, v, lens, lens)
+    # one token's keys for all (stride 0) are refused
+    with pytest.raises(kvq.KvqError):
+        kvq.prompt_attention(q, k[:1].expand(t, 2, 128), v, i32(cu(lens)))
 
 
 @pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
