@@ -345,8 +345,9 @@ KVQ_API kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k
 /* k_cache, v_cache   [num_pages, block, Nkv, D], int8 or q's type; only the  */
 /*          page dimension strided (a multiple of 16 bytes), 16-byte aligned. */
 /* scale_k, scale_v   f32, Nkv*D elements, required for int8 caches:          */
-/* offset_k, offset_v value = (code - offset) * scale; offsets optional.      */
-/*          NULL (else KVQ_ERR_ATTR) for 16-bit caches.                        */
+/* offset_k, offset_v value = (code - offset) * scale; offsets optional;      */
+/*          scale_k and offset_k 16-byte aligned.  NULL (else KVQ_ERR_ATTR)   */
+/*          for 16-bit caches.                                                 */
 /* block_table   int32 [B, cols], columns contiguous, any row stride (0 too): */
 /*          the pages of each request's own tokens, which follow the prefix.  */
 /* seq_lens int32 [B]: own tokens of each request, 0 .. cols * block; -1: the */
@@ -360,8 +361,10 @@ KVQ_API kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k
 /*          0), 16-byte aligned; its contents need no initialisation and mean */
 /*          nothing afterwards.  Calls that may run at the same time need one */
 /*          each.                                                              */
-/* Arithmetic as prompt_attention's; int8 codes enter the products exactly    */
-/* and the scales in fp32.                                                     */
+/* Arithmetic as prompt_attention's.  int8 codes enter the products exactly,  */
+/* as f16; q times the key scale is rounded to f16 relative to the row's      */
+/* largest (for f16 q to a sum of two f16 values), the weights to f16; the    */
+/* value scale and offset are applied in fp32.  Two kernels on `stream`.      */
 /* ------------------------------------------------------------------------ */
 KVQ_API kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_cache,
                                                const kvq_tensor* v_cache, const kvq_tensor* block_table,

@@ -3,7 +3,7 @@
 #include "kvq_host.cuh"
 #include "attention_common.cuh"
 #include "attention_prompt.cuh"
-#include "attention_simple.cuh"
+#include "attention_shared.cuh"
 
 namespace kvq {
 unsigned int* attention_fault_word() {
@@ -86,6 +86,52 @@ kvq_status run_prompt(const PromptArgs& a, cudaStream_t s) {
                            mv, a));
 }
 
+// How the work is laid out, and the workspace in bytes.  The size is that of
+// two-tile groups in either form (a one-tile group needs half the rows, twice
+// the groups), for as many CTAs as the kernel ever has.
+int64_t shared_plan(int64_t B, int64_t Nq, int64_t Nkv, int64_t D, int64_t prefix_len, bool hilo, SharedPlan* p) {
+    const int64_t G = Nq / Nkv, tok = 128 / G;
+    auto area = [&](int64_t group, int64_t* slots, int64_t* rows) {
+        *slots = prefix_len > 0 ? ((B + group - 1) / group) * Nkv + SA_MAX_CTAS : 0;
+        *rows = (B < tok ? B : tok) * G;
+        return *slots * 2 * *rows;
+    };
+    int64_t slots, rows;
+    const int64_t group = hilo ? tok : 2 * tok;
+    const int64_t pre = area(tok, &slots, &rows);                   // rows of the prefix slots, the larger form
+    area(group, &slots, &rows);
+    const int64_t own = (B * Nkv + SA_MAX_CTAS) * 2 * G;
+    p->group = (int32_t)group;
+    p->n_groups = (int32_t)((B + group - 1) / group);
+    p->blocks = (int32_t)((prefix_len + SA_KEYS - 1) / SA_KEYS);
+    p->last_alt = hilo || B - (p->n_groups - 1) * group <= tok;
+    p->tile_rows = (int32_t)rows;
+    p->own_area = pre * D;
+    p->stats_area = (pre + own) * D;
+    p->own_stats = p->stats_area + 2 * pre;
+    p->hilo = hilo;
+    return (p->own_stats + 2 * own) * 4;
+}
+
+template <int T, int C, int D>
+kvq_status run_shared(const SharedArgs& a, cudaStream_t s) {
+    constexpr bool I8 = C == ATT_I8;
+    SharedPlan p;
+    shared_plan(a.B, a.Nq, a.Nkv, D, a.prefix_len, I8 && T == ATT_F16, &p);
+    p.cost_own = I8 ? SA_COST_OWN8 : SA_COST_OWN16;
+    CUtensorMap mq = {}, mq1 = {};
+    if (!I8 && (!rows_map(&mq, T, a.q, a.B, a.Nq, D, a.G, 128 / a.G) || !rows_map(&mq1, T, a.q, a.B, a.Nq, D, a.G, 1)))
+        return KVQ_ERR_CUDA;
+    // at most one CTA per step that the lengths can ask for
+    const int64_t steps = (int64_t)p.n_groups * a.Nkv * p.blocks +
+                          (int64_t)a.B * a.Nkv * (((int64_t)a.cols * a.block + SA_KEYS - 1) / SA_KEYS);
+    auto kernel = shared_kernel<T, C, D>;
+    constexpr uint32_t smem = sa_smem_bytes(D, I8);
+    const int64_t ctas = persistent_grid(kernel, SA_THREADS, steps < SA_MAX_CTAS ? steps : SA_MAX_CTAS, smem);
+    if (steps > 0 && launch(kernel, (unsigned)ctas, SA_THREADS, smem, s, mq, mq1, a, p) != cudaSuccess) return KVQ_ERR_CUDA;
+    return launched(launch(shared_join_kernel<T, C, D>, (unsigned)a.B, SJ_THREADS, 0, s, a, p, (int)ctas));
+}
+
 }  // namespace
 
 extern "C" {
@@ -165,9 +211,11 @@ kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k, const 
 
 int64_t kvq_shared_prefix_attention_workspace(int64_t batch, int64_t n_q, int64_t n_kv, int64_t dim,
                                               int64_t prefix_len, int64_t max_own) {
-    if (batch < 0 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || (dim != 64 && dim != 128) || prefix_len < 0 || max_own < 0)
+    if (batch < 0 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || n_q / n_kv > 128 || (dim != 64 && dim != 128) ||
+        prefix_len < 0 || max_own < 0 || batch > ATT_MAX_TOKENS / n_q || max_own + prefix_len > ATT_MAX_TOKENS)
         return -1;
-    return 0;
+    SharedPlan p;
+    return shared_plan(batch, n_q, n_kv, dim, prefix_len, false, &p);
 }
 
 kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_cache, const kvq_tensor* v_cache,
@@ -263,7 +311,7 @@ kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_
     for (int i = 0; i < 4; ++i)
         if (par[i] && !pp[i]) return KVQ_ERR_NULL;
     if (!aligned16(q->data) || !aligned16(out->data) || !aligned16(k_cache->data) || !aligned16(v_cache->data) ||
-        !aligned16(a.workspace))
+        !aligned16(pp[0]) || !aligned16(pp[2]) || !aligned16(a.workspace))
         return KVQ_ERR_LAYOUT;
     a.k_cache = static_cast<const uint8_t*>(k_cache->data);
     a.v_cache = static_cast<const uint8_t*>(v_cache->data);
@@ -290,8 +338,7 @@ kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_
     a.D = (int32_t)D;
     a.scale = softmax_scale;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    auto go = [&](auto kernel) { return launched(launch(kernel, (unsigned)((B * Nq + 3) / 4), 128, 0, s, a)); };
-#define KVQ_SHARED(T, C) (D == 64 ? go(shared_simple_kernel<T, C, 64>) : go(shared_simple_kernel<T, C, 128>))
+#define KVQ_SHARED(T, C) (D == 64 ? run_shared<T, C, 64>(a, s) : run_shared<T, C, 128>(a, s))
     if (type == ATT_BF16) return i8 ? KVQ_SHARED(ATT_BF16, ATT_I8) : KVQ_SHARED(ATT_BF16, ATT_BF16);
     return i8 ? KVQ_SHARED(ATT_F16, ATT_I8) : KVQ_SHARED(ATT_F16, ATT_F16);
 #undef KVQ_SHARED

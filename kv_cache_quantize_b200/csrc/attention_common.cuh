@@ -11,6 +11,9 @@
 namespace kvq {
 
 constexpr float ATT_LOG2E = 1.4426950408889634f;
+// f16 weights are scaled up by 2^8, so that weights down to 2^-22 of the
+// largest stay normal numbers; with a slack of 2^7 they stay below 65504
+constexpr float ATT_F16_SHIFT = 8.0f;
 constexpr float ATT_LN2 = 0.6931471805599453f;
 
 // element types of queries, outputs and 16-bit caches; ATT_I8: int8 caches
@@ -89,19 +92,6 @@ struct SharedArgs {
     uint8_t* workspace;
 };
 
-// The page that holds token t of a page list, or -1 (FAULT_SLOT_RANGE) when
-// the entry is not a page; *in_page receives the token's place in it.
-__device__ __forceinline__ int32_t page_of(const SharedArgs& a, const int32_t* list, int32_t t, int32_t* in_page) {
-    const int32_t e = a.block_shift >= 0 ? t >> a.block_shift : t / a.block;
-    *in_page = t - e * a.block;
-    const int32_t p = __ldg(list + e);
-    if (p < 0 || p >= a.num_pages) {
-        raise_fault(FAULT_SLOT_RANGE);
-        return -1;
-    }
-    return p;
-}
-
 // Request b's own length: -1 for a row that takes no part; a length that its
 // table row cannot hold sets FAULT_SLOT_RANGE and counts as -1.
 __device__ __forceinline__ int32_t own_length(const SharedArgs& a, int b) {
@@ -126,10 +116,51 @@ __device__ __forceinline__ void att_store(uint8_t* p, int64_t i, float v) {
     else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
-#pragma unroll
-    for (int d = 16; d > 0; d >>= 1) v = __fadd_rn(v, __shfl_xor_sync(FULL_MASK, v, d));
-    return v;
+// the exponent bits of two packed 16-bit values: nonzero where one is not finite
+template <int T>
+__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
+    constexpr uint32_t E = T == ATT_BF16 ? 0x7F807F80u : 0x7C007C00u;
+    const uint32_t x = (w & E) ^ E;
+    return ((x & 0xFFFFu) == 0u ? 0xFFFFu : 0u) | ((x >> 16) == 0u ? 0xFFFF0000u : 0u);
+}
+
+template <int T>
+__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
+    uint32_t r;
+    if (T == ATT_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
+    return r;
+}
+__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
 }
 
 }  // namespace kvq

@@ -24,7 +24,7 @@
 //
 // A row's weights are rounded to the 16-bit type of V for the product (half a
 // step, the rounding that the output itself gets); their sum is taken before.
-// f16 weights are scaled up by 2^PA_F16_SHIFT so that small ones stay normal.
+// f16 weights are scaled up by 2^ATT_F16_SHIFT so that small ones stay normal.
 //
 // A masked key has weight 0, but 0 * NaN is NaN: V rows behind the sequence's
 // last key are zeroed in shared memory, and in blocks that some row of the
@@ -41,7 +41,6 @@ constexpr int PA_THREADS = 384;                    // 8 softmax warps, MMA, load
 constexpr int PA_KEYS = 128;                       // keys of a block
 constexpr int PA_ITEMS = 2;                        // work item slots
 constexpr float PA_SLACK = 7.0f;                   // log2 of how far above the reference a weight may get
-constexpr float PA_F16_SHIFT = 8.0f;               // 2^(8 + 7) < 65504
 constexpr uint64_t PA_WAIT_NS = 2000000000ull;     // every wait gives up after 2 s
 
 __host__ __device__ constexpr int pa_stages(int D) { return D == 128 ? 5 : 8; }
@@ -59,53 +58,6 @@ struct PromptItem {
     int32_t kh;              // key head
     int32_t dirty;           // values that are not finite were taken out of V
 };
-
-// the exponent bits of two packed 16-bit values: nonzero where one is not finite
-template <int T>
-__device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
-    constexpr uint32_t E = T == ATT_BF16 ? 0x7F807F80u : 0x7C007C00u;
-    const uint32_t x = (w & E) ^ E;
-    return ((x & 0xFFFFu) == 0u ? 0xFFFFu : 0u) | ((x >> 16) == 0u ? 0xFFFF0000u : 0u);
-}
-
-template <int T>
-__device__ __forceinline__ uint32_t pack2(float lo, float hi) {
-    uint32_t r;
-    if (T == ATT_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-    float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-    return d;
-}
-
-__device__ __forceinline__ float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-__device__ __forceinline__ uint64_t f32x2(float lo, float hi) {
-    uint64_t r;
-    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-    return r;
-}
-__device__ __forceinline__ void f32x2_split(uint64_t v, float& lo, float& hi) {
-    asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-    uint64_t d;
-    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-    return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
 
 template <int T, int D>
 __global__ void __launch_bounds__(PA_THREADS, 1)
@@ -354,7 +306,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         const int rt = r / a.G, g = r - rt * a.G;
         const float c = fmaxf(fabsf(a.scale) * ATT_LOG2E, 1.17549435e-38f);          // not 0: -inf stays -inf
         const uint32_t flip = a.scale < 0.0f ? 0x80000000u : 0u;
-        constexpr float SHIFT = T == ATT_F16 ? PA_F16_SHIFT : 0.0f;
+        constexpr float SHIFT = T == ATT_F16 ? ATT_F16_SHIFT : 0.0f;
         uint32_t pos = 0, s_n = 0, o_n = 0;
         bool ok = true;
         for (uint32_t n_item = 0; ok; ++n_item) {

@@ -1,0 +1,825 @@
+// attention_shared.cuh -- attention of one token per request over a paged
+// cache, for a batch that shares a prefix.
+//
+// The prefix is one product for the whole batch: the rows of a query tile are
+// 128 / G requests x the G query heads of a key head, and every key of the
+// prefix is read once for all of them (compute bound from some hundred rows
+// on).  A request's own keys are read for its G rows alone (memory bound).
+// Both run on the tensor cores in one persistent kernel (tcgen05, as the
+// prompt kernel), and a second one joins the partial results.
+//
+// Work is a row of steps of 128 keys: the prefix of each group of requests and
+// key head, then each request's own keys for each key head.  The row is cut
+// into equal parts by cost, one for each CTA, wherever the cuts fall, so all
+// CTAs end together whatever the lengths are.  A piece of a group on a CTA
+// leaves its unnormalised output, maximum and sum in the workspace, at slot
+// (group + CTA): that number grows along the row, so no two pieces share it.
+//
+// Two query tiles are in flight per CTA, one in its softmax while the tensor
+// core works on the other.  A group of up to 128 rows has only one tile of
+// rows: both tiles then hold the same rows and take the steps in turn.
+//
+//   warps 0-3, 4-7   softmax of tile 0 and 1, a thread per row;
+//   warps 8-11       keys and values: 16-byte asynchronous copies through the
+//                    page lists, any page size; int8 codes are turned into f16
+//                    (exactly) on their way into the product's tiles;
+//   warp 12          one lane issues tcgen05.mma;
+//   warp 13          cuts the work, and loads Q where it needs no scaling.
+//
+// int8 caches: value = (code - offset) * scale per channel.  q is multiplied
+// by the key scale in fp32, scaled by a power of two per row to f16's range
+// and rounded to f16 -- one value for bf16 queries (2^-11, an eighth of their
+// own half step), a sum of two for f16 queries (2^-22).  The key offset adds
+// the same to all scores of a row and only enters lse; the value scale and
+// offset are applied to the joined output.
+#pragma once
+
+#include "attention_common.cuh"
+#include "tcgen05.cuh"
+
+namespace kvq {
+
+constexpr int SA_THREADS = 512;
+constexpr int SA_KEYS = 128;
+constexpr int SA_ITEMS = 3;
+constexpr int SA_MAX_CTAS = 148;
+constexpr int SA_BAD = 8;                          // blocks whose missing keys are remembered
+constexpr float SA_SLACK = 7.0f;
+constexpr uint64_t SA_WAIT_NS = 2000000000ull;
+
+// tiles of the ring of keys and values (f16 or bf16), raw int8 tiles behind
+// it, and copies in flight; 224 KB with the two query tiles at D = 128
+__host__ __device__ constexpr int sa_ring(bool i8) { return i8 ? 3 : 5; }
+__host__ __device__ constexpr int sa_lag(bool i8) { return i8 ? 3 : 2; }
+__host__ __device__ constexpr uint32_t sa_tile_bytes(int D) { return 128u * (uint32_t)D * 2u; }
+__host__ __device__ constexpr uint32_t sa_smem_bytes(int D, bool i8) {
+    return (2u + (uint32_t)sa_ring(i8)) * sa_tile_bytes(D) + (i8 ? (uint32_t)(sa_lag(i8) + 1) * sa_tile_bytes(D) / 2u : 0u) +
+           512u + SA_BAD * 128u + 1024u;           // + barriers and items, key flags, alignment
+}
+
+// the cost of a step: two tiles of rows, one tile (prefix), a request's own
+// keys (int8, 16-bit)
+constexpr int SA_COST2 = 3, SA_COST1 = 2, SA_COST_OWN8 = 2, SA_COST_OWN16 = 3;
+
+struct SharedPlan {
+    int32_t group;           // requests of a prefix group
+    int32_t n_groups;        // groups of requests
+    int32_t blocks;          // prefix steps of a group
+    int32_t cost_own;
+    int32_t last_alt;        // the last group of requests has one tile of rows
+    int32_t tile_rows;       // rows of a tile in a prefix slot
+    int64_t own_area;        // floats before the own slots
+    int64_t stats_area;      // floats before the (maximum, sum) pairs of the prefix slots; own_stats behind
+    int64_t own_stats;
+    int32_t hilo;
+};
+
+struct SharedItem {
+    int32_t steps;           // -1: no more work
+    int32_t alt;             // both tiles hold the same rows and take the steps in turn
+    int32_t own;             // a request's own keys
+    int32_t b0, nreq;        // requests
+    int32_t kh;
+    int32_t key0, keys;      // first key of the list, keys in all
+    int32_t slot;
+};
+
+// ceil(x / k) for x of either sign, k > 0
+__device__ __forceinline__ int64_t ceil_div(int64_t x, int64_t k) { return x > 0 ? (x + k - 1) / k : -((-x) / k); }
+
+__device__ __forceinline__ int32_t own_blocks(const SharedArgs& a, int b) {
+    const int32_t n = __ldg(a.seq_lens + b);
+    return n > 0 && n <= (int64_t)a.cols * a.block ? (n + SA_KEYS - 1) / SA_KEYS : 0;
+}
+
+// where prefix group (pt, kh) starts in the row of work, and a step's cost
+__device__ __forceinline__ int64_t prefix_start(const SharedArgs& a, const SharedPlan& p, int pt, int kh, int* k) {
+    const bool last = pt == p.n_groups - 1;
+    const int full = p.hilo ? SA_COST1 : SA_COST2;
+    *k = last && p.last_alt ? SA_COST1 : full;
+    return ((int64_t)pt * a.Nkv * full + (int64_t)kh * *k) * p.blocks;
+}
+__device__ __forceinline__ int64_t prefix_cost(const SharedArgs& a, const SharedPlan& p) {
+    if (p.blocks == 0) return 0;
+    int k;
+    const int64_t s = prefix_start(a, p, p.n_groups - 1, a.Nkv - 1, &k);
+    return s + (int64_t)k * p.blocks;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
+
+// four int8 codes -> four f16 values: 1024 + (code + 128) is an f16 whose low
+// byte is the code with its sign bit flipped
+__device__ __forceinline__ void i8x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    const uint32_t x = w ^ 0x80808080u;
+    const __half2 bias = __halves2half2(__ushort_as_half(0x6480), __ushort_as_half(0x6480));
+    uint32_t l = __byte_perm(x, 0x64646464u, 0x4140), h = __byte_perm(x, 0x64646464u, 0x4342);
+    __half2 a = __hsub2(*reinterpret_cast<__half2*>(&l), bias), b = __hsub2(*reinterpret_cast<__half2*>(&h), bias);
+    lo = *reinterpret_cast<uint32_t*>(&a);
+    hi = *reinterpret_cast<uint32_t*>(&b);
+}
+
+// position of step s's keys and values in the order K0 K1 V0 K2 V1 ... V(n-1)
+__device__ __forceinline__ uint32_t k_pos(int s) { return s == 0 ? 0u : 2u * s - 1u; }
+__device__ __forceinline__ uint32_t v_pos(int s, int n) { return s == n - 1 ? 2u * n - 1u : 2u * s + 2u; }
+
+template <int T, int C, int D>
+__global__ void __launch_bounds__(SA_THREADS, 1)
+    shared_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
+                  const __grid_constant__ SharedArgs a, const __grid_constant__ SharedPlan plan) {
+    constexpr bool I8 = C == ATT_I8;
+    constexpr int MT = I8 ? ATT_F16 : T;                     // type of the products
+    constexpr bool HILO = I8 && T == ATT_F16;
+    constexpr int NS = sa_ring(I8), LAG = sa_lag(I8), NR = LAG + 1;
+    constexpr int PANELS = D / 64;
+    constexpr uint32_t TILE = sa_tile_bytes(D), PANEL = 128 * 128, O_COL = 256;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint8_t* q_s = smem;
+    uint8_t* kv_s = smem + 2 * TILE;
+    uint8_t* raw_s = smem + (2 + NS) * TILE;
+    uint8_t* after = raw_s + (I8 ? NR * (TILE / 2) : 0);
+    uint8_t* key_ok = after;                                 // [SA_BAD][128]
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(after + SA_BAD * 128);
+    uint64_t* q_empty = q_full + 2;
+    uint64_t* s_full = q_empty + 2;
+    uint64_t* p_ready = s_full + 2;
+    uint64_t* o_full = p_ready + 2;
+    uint64_t* item_full = o_full + 2;
+    uint64_t* item_empty = item_full + SA_ITEMS;
+    uint64_t* kv_full = item_empty + SA_ITEMS;
+    uint64_t* kv_empty = kv_full + NS;
+    uint64_t* drain = kv_empty + NS;
+    uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
+    volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);      // [SA_BAD]
+    volatile SharedItem* items = reinterpret_cast<volatile SharedItem*>(tmem_slot + 2 + SA_BAD);
+    int* s_blocks = reinterpret_cast<int*>(tmem_slot + 1);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int TOK = 128 / a.G;
+
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], I8 ? 128 : 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+            mbar_init(&p_ready[i], 128);
+            mbar_init(&o_full[i], 1);
+        }
+        for (int i = 0; i < SA_ITEMS; ++i) {
+            mbar_init(&item_full[i], 1);
+            mbar_init(&item_empty[i], 13);                   // 8 softmax and 4 load warps, the MMA lane
+        }
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&kv_full[i], 128);
+            mbar_init(&kv_empty[i], 1);
+        }
+        mbar_init(drain, 1);
+        mbar_init_fence();
+        *s_blocks = 0;
+        for (int i = 0; i < SA_BAD; ++i) bad[i] = 0u;
+    }
+    if (warp == 12) tm_alloc(tmem_slot, 512);
+    tm_fence_before();
+    __syncthreads();
+    tm_fence_after();
+    const uint32_t tmem = *tmem_slot;
+    pdl_wait();
+    pdl_trigger();
+    // all requests' own steps
+    {
+        int n = 0;
+        for (int b = threadIdx.x; b < a.B; b += SA_THREADS) n += own_blocks(a, b);
+        n = __reduce_add_sync(FULL_MASK, n);
+        if (lane == 0 && n) atomicAdd(s_blocks, n);
+    }
+    __syncthreads();
+    const int64_t pre_cost = prefix_cost(a, plan);
+    const int64_t total = pre_cost + (int64_t)*s_blocks * a.Nkv * plan.cost_own;
+    const int64_t width = (total + gridDim.x - 1) / gridDim.x;
+
+    // 512 threads x 128 registers at launch, split 256 x 160 + 128 x 120 + 128 x 72
+    if (warp == 13) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---------------- work, and Q where TMA can bring it ----------------
+        uint32_t n_item = 0, q_n[2] = {0, 0};
+        const int64_t hi = min((int64_t)(blockIdx.x + 1) * width, total);
+        int64_t at = (int64_t)blockIdx.x * width;
+        int cb = 0;                                          // cursor over the requests
+        int64_t cstart = pre_cost;
+        bool dead = false;
+        while (!dead) {
+            SharedItem w;
+            w.steps = -1;
+            while (at < hi && w.steps <= 0) {
+                int64_t gs;
+                int32_t blocks, len, g;
+                int k;
+                if (at < pre_cost) {
+                    const int full = HILO ? SA_COST1 : SA_COST2;
+                    int pt = (int)(at / ((int64_t)plan.blocks * a.Nkv * full));
+                    if (pt > plan.n_groups - 1) pt = plan.n_groups - 1;
+                    gs = prefix_start(a, plan, pt, 0, &k);
+                    const int kh = (int)((at - gs) / ((int64_t)k * plan.blocks));
+                    gs += (int64_t)kh * k * plan.blocks;
+                    w.own = 0;
+                    w.b0 = pt * plan.group;
+                    w.nreq = min(plan.group, a.B - w.b0);
+                    w.alt = HILO || w.nreq <= TOK;
+                    w.kh = kh;
+                    blocks = plan.blocks;
+                    len = a.prefix_len;
+                    g = pt * a.Nkv + kh;
+                } else {
+                    // the request whose steps hold this place
+                    bool found = false;
+                    k = plan.cost_own;
+                    blocks = 0;
+                    gs = 0;
+                    w.b0 = 0;
+                    while (!found && cb < a.B) {
+                        const int32_t nb = cb + lane < a.B ? own_blocks(a, cb + lane) : 0;
+                        int32_t incl = nb;
+#pragma unroll
+                        for (int d = 1; d < 32; d <<= 1) {
+                            const int32_t y = __shfl_up_sync(FULL_MASK, incl, d);
+                            if (lane >= d) incl += y;
+                        }
+                        const unsigned past = __ballot_sync(FULL_MASK, cstart + (int64_t)incl * a.Nkv * k > at);
+                        if (past) {
+                            const int src = __ffs(past) - 1;
+                            found = true;
+                            w.b0 = cb + src;
+                            blocks = __shfl_sync(FULL_MASK, nb, src);
+                            gs = cstart + (int64_t)(__shfl_sync(FULL_MASK, incl, src) - blocks) * a.Nkv * k;
+                        } else {
+                            cstart += (int64_t)__shfl_sync(FULL_MASK, incl, 31) * a.Nkv * k;
+                            cb += 32;
+                        }
+                    }
+                    if (!found) break;
+                    w.kh = (int)((at - gs) / ((int64_t)k * blocks));
+                    gs += (int64_t)w.kh * k * blocks;
+                    w.own = 1;
+                    w.nreq = 1;
+                    w.alt = 1;
+                    len = __ldg(a.seq_lens + w.b0);
+                    g = w.b0 * a.Nkv + w.kh;
+                }
+                const int64_t s0 = max(ceil_div((int64_t)blockIdx.x * width - gs, k), (int64_t)0);
+                const int64_t s1 = min(ceil_div(hi - gs, k), (int64_t)blocks);
+                at = gs + (int64_t)k * blocks;
+                if (s1 > s0) {
+                    w.steps = (int32_t)(s1 - s0);
+                    w.key0 = (int32_t)s0 * SA_KEYS;
+                    w.keys = min(len - w.key0, w.steps * SA_KEYS);
+                    w.slot = g + (int)blockIdx.x;
+                }
+            }
+            const uint32_t slot = n_item % SA_ITEMS;
+            if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_empty[slot], ((n_item / SA_ITEMS) & 1u) ^ 1u, SA_WAIT_NS))) break;
+            if (lane == 0) {
+                volatile SharedItem& o = items[slot];
+                o.steps = w.steps;
+                o.alt = w.alt;
+                o.own = w.own;
+                o.b0 = w.b0;
+                o.nreq = w.nreq;
+                o.kh = w.kh;
+                o.key0 = w.key0;
+                o.keys = w.keys;
+                o.slot = w.slot;
+                mbar_arrive(&item_full[slot]);
+            }
+            __syncwarp();
+            ++n_item;
+            if (w.steps < 0) break;
+            if (!I8 && lane == 0) {
+                for (int i = 0; i < 2 && !dead; ++i) {
+                    if (i == 1 && w.alt && w.steps == 1) continue;
+                    if (!mbar_wait_ns(&q_empty[i], (q_n[i] & 1u) ^ 1u, SA_WAIT_NS)) {
+                        dead = true;
+                        break;
+                    }
+                    ++q_n[i];
+                    mbar_arrive_expect_tx(&q_full[i], (uint32_t)(w.own ? a.G : TOK * a.G) * 128u * PANELS);
+                    for (int p = 0; p < PANELS; ++p) {
+                        uint8_t* dst = q_s + i * TILE + p * PANEL;
+                        // a request's own rows: lanes 32 .. in tile 1, so that the two tiles' softmax
+                        // warps sit on different schedulers
+                        if (w.own) tma_load_3d(dst + (i && a.G <= 96 ? 32 * 128 : 0), &tm_q1, 64 * p, w.kh * a.G, w.b0, &q_full[i]);
+                        else tma_load_3d(dst, &tm_q, 64 * p, w.kh * a.G, w.b0 + (w.alt ? 0 : i * TOK), &q_full[i]);
+                    }
+                }
+            }
+            dead = __shfl_sync(FULL_MASK, dead, 0);
+        }
+        if (!I8 && lane == 0)
+            for (int i = 0; i < 2; ++i)
+                if (q_n[i] > 0) mbar_wait_ns(&q_full[i], (q_n[i] - 1) & 1u, SA_WAIT_NS);
+    } else if (warp == 12) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---------------- tensor-core products ----------------
+        if (lane == 0) {
+            constexpr bool BF = MT == ATT_BF16;
+            constexpr uint32_t ID_S = umma_idesc(BF, false, 128, SA_KEYS), ID_O = umma_idesc(BF, true, 128, D);
+            uint32_t pos = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0};
+            auto wait_kv = [&](uint32_t k) { return mbar_wait_ns(&kv_full[k % NS], (k / NS) & 1u, SA_WAIT_NS); };
+            auto scores = [&](int i, uint32_t k) {
+                const uint32_t ka = smem_u32(kv_s + (k % NS) * TILE);
+                tm_fence_after();
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    const uint32_t off = (d / 4) * PANEL + (d % 4) * 32;
+                    const uint64_t kd = umma_desc_k(ka + off);
+                    umma_ss(tmem + 128 * i, umma_desc_k(smem_u32(q_s + (HILO ? 0 : i) * TILE) + off), kd, ID_S, d != 0);
+                    if (HILO) umma_ss(tmem + 128 * i, umma_desc_k(smem_u32(q_s + TILE) + off), kd, ID_S, true);
+                }
+                umma_done(&s_full[i]);
+            };
+            auto values = [&](int i, uint32_t k, bool first) {
+                const uint32_t va = smem_u32(kv_s + (k % NS) * TILE);
+                tm_fence_after();
+#pragma unroll
+                for (int d = 0; d < SA_KEYS / 16; ++d)
+                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, umma_desc_mn(va + 2048 * d, PANEL), ID_O,
+                            !first || d != 0);
+            };
+            bool ok = true;
+            for (uint32_t n_item = 0; ok; ++n_item) {
+                const uint32_t slot = n_item % SA_ITEMS;
+                if (!mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS)) break;
+                const int n = items[slot].steps;
+                const bool alt = items[slot].alt != 0;
+                mbar_arrive(&item_empty[slot]);
+                if (n < 0) break;
+                // the first scores of each tile
+                for (int i = 0; i < 2 && ok; ++i) {
+                    const int s = alt ? i : 0;
+                    if (s >= n) break;
+                    if (!HILO || i == 0) ok = mbar_wait_ns(&q_full[i], q_n[i]++ & 1u, SA_WAIT_NS);
+                    ok = ok && wait_kv(pos + k_pos(s));
+                    if (!ok) break;
+                    scores(i, pos + k_pos(s));
+                    if (alt) umma_done(&kv_empty[(pos + k_pos(s)) % NS]);
+                    if (!HILO && (alt ? s + 2 >= n : n == 1)) umma_done(&q_empty[i]);
+                }
+                if (ok && !alt) umma_done(&kv_empty[pos % NS]);
+                for (int s = 0; s < n && ok; ++s) {
+                    const uint32_t v = pos + v_pos(s, n);
+                    ok = wait_kv(v);
+                    for (int i = alt ? s & 1 : 0; i < (alt ? (s & 1) + 1 : 2) && ok; ++i) {
+                        ok = mbar_wait_ns(&p_ready[i], p_n[i]++ & 1u, SA_WAIT_NS);
+                        if (!ok) break;
+                        values(i, v, s < (alt ? 2 : 1));
+                        const int nx = s + (alt ? 2 : 1);
+                        if (nx >= n) {
+                            umma_done(&o_full[i]);
+                        } else {
+                            const uint32_t k = pos + k_pos(nx);
+                            ok = wait_kv(k);
+                            if (!ok) break;
+                            scores(i, k);
+                            if (alt || i == 1) umma_done(&kv_empty[k % NS]);
+                            if (!HILO && nx + (alt ? 2 : 1) >= n) umma_done(&q_empty[i]);
+                        }
+                    }
+                    if (ok) umma_done(&kv_empty[v % NS]);
+                }
+                if (HILO && ok) umma_done(&q_empty[0]);
+                pos += 2 * n;
+            }
+            umma_done(drain);
+            mbar_wait_ns(drain, 0u, SA_WAIT_NS);
+        }
+    } else if (warp >= 14) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    } else if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
+        // ---------------- keys and values ----------------
+        const int p = threadIdx.x - 256;
+        constexpr int EB = I8 ? 1 : 2;
+        constexpr int CH = D * EB / 16;                      // 16-byte pieces of a row
+        constexpr int RP = 128 / CH;                         // rows of a pass
+        constexpr int PASSES = 128 / RP;
+        const int ch = p % CH, r0 = p / CH;
+        const int64_t row_bytes = (int64_t)a.Nkv * D * EB;
+        uint32_t issued = 0, done = 0, block_no = 0;
+        bool ok = true;
+        auto finish = [&]() {
+            if (I8) {
+                // this thread's own copies have arrived: codes to f16
+                ok = __all_sync(FULL_MASK, mbar_wait_ns(&kv_empty[done % NS], ((done / NS) & 1u) ^ 1u, SA_WAIT_NS));
+                if (!ok) return;
+                const uint8_t* src = raw_s + (done % NR) * (TILE / 2) + p * 16;
+                uint8_t* dst = kv_s + (done % NS) * TILE + (ch / 4) * PANEL;
+                const int c0 = 2 * (ch & 3);
+                const int first = (ch >> 2) & 1;             // panel 1 starts with the other half: no bank conflict
+#pragma unroll
+                for (int k = 0; k < PASSES; ++k) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(src + k * 2048);
+                    const int r = r0 + k * RP;
+                    uint4 h[2];
+                    i8x4_f16(w.x, h[0].x, h[0].y);
+                    i8x4_f16(w.y, h[0].z, h[0].w);
+                    i8x4_f16(w.z, h[1].x, h[1].y);
+                    i8x4_f16(w.w, h[1].z, h[1].w);
+                    uint8_t* row = dst + r * 128;
+                    const uint4 e0 = first ? h[1] : h[0], e1 = first ? h[0] : h[1];
+                    *reinterpret_cast<uint4*>(row + (((c0 + first) ^ (r & 7)) << 4)) = e0;
+                    *reinterpret_cast<uint4*>(row + (((c0 + (first ^ 1)) ^ (r & 7)) << 4)) = e1;
+                }
+            }
+            fence_proxy_async_smem();
+            mbar_arrive(&kv_full[done % NS]);
+            ++done;
+        };
+        for (uint32_t n_item = 0; ok; ++n_item) {
+            const uint32_t slot = n_item % SA_ITEMS;
+            if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
+            const int n = items[slot].steps, own = items[slot].own, b0 = items[slot].b0, kh = items[slot].kh;
+            const int key0 = items[slot].key0, keys = items[slot].keys;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[slot]);
+            if (n < 0) break;
+            const int32_t* list = own ? a.table + (int64_t)b0 * a.table_stride : a.prefix_table;
+            const int64_t head = (int64_t)kh * D * EB + ch * 16;
+            for (int q = 0; q < 2 * n && ok; ++q) {
+                // the order K0 K1 V0 K2 V1 ... V(n-1)
+                const bool is_v = q > 0 && ((q & 1) == 0 || q == 2 * n - 1);
+                const int s = q == 0 ? 0 : is_v ? (q == 2 * n - 1 ? n - 1 : (q - 2) / 2) : (q + 1) / 2;
+                if (!I8) {
+                    ok = __all_sync(FULL_MASK, mbar_wait_ns(&kv_empty[issued % NS], ((issued / NS) & 1u) ^ 1u, SA_WAIT_NS));
+                    if (!ok) break;
+                }
+                const uint8_t* base = (is_v ? a.v_cache : a.k_cache) + head;
+                const int64_t page_bytes = is_v ? a.v_page : a.k_page;
+                const uint32_t dst = I8 ? smem_u32(raw_s + (issued % NR) * (TILE / 2) + p * 16)
+                                        : smem_u32(kv_s + (issued % NS) * TILE + (ch / 8) * PANEL);
+                const uint32_t nb = block_no % SA_BAD;
+#pragma unroll
+                for (int k = 0; k < PASSES; ++k) {
+                    const int r = r0 + k * RP;
+                    const int t = s * SA_KEYS + r;           // key of the piece
+                    const uint8_t* src = base;
+                    uint32_t bytes = 0;
+                    if (t < keys) {
+                        const int32_t tok = key0 + t;
+                        const int32_t e = a.block_shift >= 0 ? tok >> a.block_shift : tok / a.block;
+                        const int32_t page = __ldg(list + e);
+                        if ((uint32_t)page < (uint32_t)a.num_pages) {
+                            src = base + page * page_bytes + (tok - e * a.block) * row_bytes;
+                            bytes = 16;
+                        }
+                        if (!is_v && ch == 0) key_ok[nb * 128 + r] = bytes != 0;
+                        if (!is_v && bytes == 0) {
+                            bad[nb] = block_no + 1;
+                            raise_fault(FAULT_SLOT_RANGE);
+                        }
+                    }
+                    cp_async16(I8 ? dst + k * 2048 : dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, bytes);
+                }
+                if (!is_v) ++block_no;
+                cp_async_commit();
+                ++issued;
+                if (issued - done > LAG) {
+                    cp_async_wait<LAG>();
+                    finish();
+                }
+            }
+        }
+        cp_async_wait<0>();
+        while (ok && done < issued) finish();
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
+        // ---------------- softmax and partial results ----------------
+        const int i = warp >> 2;
+        const int r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t s_t = tmem + lanes + 128 * i, o_t = tmem + lanes + O_COL + D * i;
+        const float c0 = fmaxf(fabsf(a.scale) * ATT_LOG2E, 1.17549435e-38f);          // not 0: -inf stays -inf
+        const uint32_t flip = a.scale < 0.0f ? 0x80000000u : 0u;
+        constexpr float SHIFT = MT == ATT_F16 ? ATT_F16_SHIFT : 0.0f;
+        float* ws = reinterpret_cast<float*>(a.workspace);
+        uint32_t s_n = 0, o_n = 0, q_n = 0, block_no = 0;
+        bool ok = true;
+        for (uint32_t n_item = 0; ok; ++n_item) {
+            const uint32_t slot = n_item % SA_ITEMS;
+            if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
+            SharedItem w;
+            w.steps = items[slot].steps;
+            w.alt = items[slot].alt;
+            w.own = items[slot].own;
+            w.b0 = items[slot].b0;
+            w.nreq = items[slot].nreq;
+            w.kh = items[slot].kh;
+            w.keys = items[slot].keys;
+            w.slot = items[slot].slot;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&item_empty[slot]);
+            if (w.steps < 0) break;
+            const int first = w.alt ? i : 0, stride = w.alt ? 2 : 1;
+            const int rows = (w.alt ? w.nreq : min(max(w.nreq - i * TOK, 0), TOK)) * a.G;
+            // a request's own rows stand at lanes 32 .. of tile 1
+            const int lr = w.own && i && !HILO && a.G <= 96 ? r - 32 : r;
+            const bool live = lr >= 0 && lr < rows;
+            const bool work = __any_sync(FULL_MASK, live);
+            float c = c0, koff = 0.0f;
+            if (I8 && first < w.steps) {
+                if (HILO && i == 0) {
+                    // both tiles read these rows: the earlier item's products are done with them
+                    ok = __all_sync(FULL_MASK, mbar_wait_ns(&q_empty[0], (q_n++ & 1u) ^ 1u, SA_WAIT_NS));
+                    if (!ok) break;
+                }
+                if (live) {
+                    const int b = w.b0 + (w.alt ? 0 : i * TOK) + (w.own ? 0 : lr / a.G);
+                    const int h = w.kh * a.G + (w.own ? lr : lr % a.G);
+                    const uint4* q = reinterpret_cast<const uint4*>(a.q.base + ((int64_t)b * a.q.tok + h * a.q.head) * 2);
+                    const float4* sk = reinterpret_cast<const float4*>(a.scale_k + w.kh * D);
+                    const float4* ok4 = reinterpret_cast<const float4*>(a.offset_k + w.kh * D);
+                    auto scaled = [&](int k, float (&x)[8]) {
+                        const uint4 e = __ldg(q + k);
+                        const float4 u = __ldg(sk + 2 * k), v = __ldg(sk + 2 * k + 1);
+                        const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
+                        const float sc[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int z = 0; z < 8; ++z)
+                            x[z] = __fmul_rn(att_load<T>(reinterpret_cast<const uint8_t*>(ew), z), sc[z]);
+                    };
+                    float top = 0.0f;
+#pragma unroll 4
+                    for (int k = 0; k < D / 8; ++k) {
+                        float x[8];
+                        scaled(k, x);
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) top = fmaxf(top, fabsf(x[z]));
+                    }
+                    const uint32_t ex = __float_as_uint(top) >> 23;                  // power of two below the maximum
+                    const bool norm = ex > 0 && ex < 254;
+                    const float down = norm ? __uint_as_float((254u - ex) << 23) : 1.0f;
+                    c = norm ? fmaxf(__fmul_rn(c0, __uint_as_float(ex << 23)), 1.17549435e-38f) : c0;
+                    const bool store = !HILO || i == 0;
+                    const bool sum = a.lse != nullptr && a.offset_k != nullptr;
+#pragma unroll 2
+                    for (int k = 0; k < D / 8; ++k) {
+                        float x[8];
+                        scaled(k, x);
+                        uint32_t hi[4], lo[4];
+                        const float4 u = sum ? __ldg(ok4 + 2 * k) : float4{}, v = sum ? __ldg(ok4 + 2 * k + 1) : float4{};
+                        const float of[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
+#pragma unroll
+                        for (int z = 0; z < 4; ++z) {
+                            const float a0 = __fmul_rn(x[2 * z], down), a1 = __fmul_rn(x[2 * z + 1], down);
+                            hi[z] = pack2<ATT_F16>(a0, a1);
+                            float h0 = __half2float(__ushort_as_half((unsigned short)(hi[z] & 0xFFFFu)));
+                            float h1 = __half2float(__ushort_as_half((unsigned short)(hi[z] >> 16)));
+                            if (HILO) {
+                                lo[z] = pack2<ATT_F16>(__fsub_rn(a0, h0), __fsub_rn(a1, h1));
+                                h0 = __fadd_rn(h0, __half2float(__ushort_as_half((unsigned short)(lo[z] & 0xFFFFu))));
+                                h1 = __fadd_rn(h1, __half2float(__ushort_as_half((unsigned short)(lo[z] >> 16))));
+                            }
+                            koff = __fmaf_rn(h0, of[2 * z], koff);
+                            koff = __fmaf_rn(h1, of[2 * z + 1], koff);
+                        }
+                        if (store) {
+                            const uint32_t off = (k / 8) * PANEL + r * 128 + (((k & 7) ^ (r & 7)) << 4);
+                            *reinterpret_cast<uint4*>(q_s + (HILO ? 0 : i) * TILE + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            if (HILO) *reinterpret_cast<uint4*>(q_s + TILE + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                        }
+                    }
+                    if (flip) koff = -koff;
+                }
+                if (!HILO || i == 0) {
+                    fence_proxy_async_smem();
+                    mbar_arrive(&q_full[i]);
+                }
+            }
+            float m = -INFINITY, l = 0.0f;
+            for (int s = first; s < w.steps; s += stride) {
+                ok = __all_sync(FULL_MASK, mbar_wait_ns(&s_full[i], s_n++ & 1u, SA_WAIT_NS));
+                if (!ok) break;
+                tm_fence_after();
+                if (work) {
+                    const int see = w.keys - s * SA_KEYS;
+                    const uint32_t blk = block_no + s;
+                    const bool gaps = bad[blk % SA_BAD] == blk + 1;
+                    // 64 scores at a time, read twice: once for the maximum, once for the weights
+                    auto load = [&](int half, uint32_t (&x)[64]) {
+                        tm_ld64(s_t + 64 * half, x);
+                        if (flip) {
+#pragma unroll
+                            for (int k = 0; k < 64; ++k) x[k] ^= flip;
+                        }
+                        if (see < 64 * half + 64) {
+#pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (64 * half + k >= see) x[k] = 0xFF800000u;
+                        }
+                        if (gaps) {
+                            const uint8_t* have = key_ok + (blk % SA_BAD) * 128 + 64 * half;
+#pragma unroll
+                            for (int k = 0; k < 64; ++k)
+                                if (!have[k]) x[k] = 0xFF800000u;
+                        }
+                    };
+                    float bm = -INFINITY;
+                    uint32_t x[64];
+#pragma unroll
+                    for (int half = 1; half >= 0; --half) {
+                        load(half, x);
+                        float mx[4] = {bm, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+                        for (int k = 0; k < 64; k += 8) {
+#pragma unroll
+                            for (int q = 0; q < 4; ++q)
+                                mx[q] = max3(mx[q], __uint_as_float(x[k + 2 * q]), __uint_as_float(x[k + 2 * q + 1]));
+                        }
+                        bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                    }
+                    const bool grow = __fmul_rn(__fsub_rn(bm, m), c) > SA_SLACK || (m == -INFINITY && bm > m);
+                    if (s == first) {
+                        m = bm;
+                    } else if (__any_sync(FULL_MASK, grow)) {
+                        const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(__fmul_rn(__fsub_rn(m, bm), c));
+                        if (grow) m = bm;
+                        l = __fmul_rn(l, f);
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
+                            tm_ld32(o_t + k, o);
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__fmul_rn(__uint_as_float(o[q]), f));
+                            tm_st32(o_t + k, o);
+                        }
+                    }
+                    const float ms = m == -INFINITY ? 0.0f : __fmaf_rn(m, c, -SHIFT);
+                    const uint64_t c2 = f32x2(c, c), ms2 = f32x2(-ms, -ms);
+                    uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        if (half) load(1, x);                 // half 0 is still here; its weights go over scores read already
+#pragma unroll
+                        for (int g = 0; g < 2; ++g) {
+                            uint32_t pk[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const uint64_t xx = fma2(f32x2(__uint_as_float(x[32 * g + 2 * k]), __uint_as_float(x[32 * g + 2 * k + 1])), c2, ms2);
+                                float lo, hi;
+                                f32x2_split(xx, lo, hi);
+                                lo = ex2(lo);
+                                hi = ex2(hi);
+                                sum[k & 1] = add2(sum[k & 1], f32x2(lo, hi));
+                                pk[k] = pack2<MT>(lo, hi);
+                            }
+                            tm_st16(s_t + 32 * half + 16 * g, pk);
+                        }
+                    }
+                    float s0, s1, s2, s3;
+                    f32x2_split(sum[0], s0, s1);
+                    f32x2_split(sum[1], s2, s3);
+                    l = __fadd_rn(l, __fadd_rn(__fadd_rn(s0, s1), __fadd_rn(s2, s3)));
+                    tm_wait_st();
+                }
+                tm_fence_before();
+                mbar_arrive(&p_ready[i]);
+            }
+            if (!ok) break;
+            block_no += w.steps;
+            if (first >= w.steps) continue;
+            ok = __all_sync(FULL_MASK, mbar_wait_ns(&o_full[i], o_n++ & 1u, SA_WAIT_NS));
+            if (!ok) break;
+            tm_fence_after();
+            if (work) {
+                const int tile_rows = w.own ? a.G : plan.tile_rows;
+                const int64_t row = ((int64_t)w.slot * 2 + i) * tile_rows + lr;
+                float* o_out = ws + (w.own ? plan.own_area : 0) + row * D;
+#pragma unroll 1
+                for (int k = 0; k < D; k += 32) {
+                    uint32_t o[32];
+                    tm_ld32(o_t + k, o);
+                    if (live) {
+#pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            reinterpret_cast<uint4*>(o_out + k)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    }
+                }
+                if (live) {
+                    float2* st = reinterpret_cast<float2*>(ws + (w.own ? plan.own_stats : plan.stats_area)) + row;
+                    // a row of NaN scores has no maximum: its sum, NaN, must still count
+                    *st = make_float2(m == -INFINITY ? (l != l ? 0.0f : m) : __fsub_rn(__fmaf_rn(m, c, -SHIFT), __fmul_rn(koff, c)), l);
+                }
+            }
+            tm_fence_before();
+        }
+    }
+    tm_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tm_fence_after();
+        tm_dealloc(tmem, 512);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Join the pieces: one warp per request and head.  Piece i: O_i, l_i relative
+// to 2^M_i; out = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i, then the value
+// scale and offset.
+// ---------------------------------------------------------------------------
+constexpr int SJ_THREADS = 256;
+
+template <int T, int C, int D>
+__global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_constant__ SharedArgs a,
+                                                                const __grid_constant__ SharedPlan plan, int ctas) {
+    constexpr bool HILO = C == ATT_I8 && T == ATT_F16;
+    constexpr int E = D / 32;
+    __shared__ int s_all, s_before;
+    const int lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) s_all = s_before = 0;
+    __syncthreads();
+    pdl_wait();
+    pdl_trigger();
+    const int b = blockIdx.x;
+    {
+        int n = 0, before = 0;
+        for (int k = threadIdx.x; k < a.B; k += SJ_THREADS) {
+            const int nb = own_blocks(a, k);
+            n += nb;
+            before += k < b ? nb : 0;
+        }
+        n = __reduce_add_sync(FULL_MASK, n);
+        before = __reduce_add_sync(FULL_MASK, before);
+        if (lane == 0) {
+            atomicAdd(&s_all, n);
+            atomicAdd(&s_before, before);
+        }
+    }
+    __syncthreads();
+    const int64_t pre_cost = prefix_cost(a, plan);
+    const int64_t total = pre_cost + (int64_t)s_all * a.Nkv * plan.cost_own;
+    const int64_t width = (total + ctas - 1) / ctas;
+    if (own_length(a, b) < 0) return;
+    const int nb = own_blocks(a, b);
+    const int TOK = 128 / a.G;
+    const float* ws = reinterpret_cast<const float*>(a.workspace);
+    for (int h = threadIdx.x >> 5; h < a.Nq; h += SJ_THREADS / 32) {
+        const int kh = h / a.G, g = h - kh * a.G;
+        float M = -INFINITY, L = 0.0f, acc[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+        auto add = [&](const float* o, float2 st) {
+            if (st.x == -INFINITY) return;
+            const float mn = fmaxf(M, st.x);
+            const float f = exp2f(__fsub_rn(M, mn)), w = exp2f(__fsub_rn(st.x, mn));
+            L = __fmaf_rn(L, f, __fmul_rn(st.y, w));
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(acc[e], f, __fmul_rn(o[lane + 32 * e], w));
+            M = mn;
+        };
+        // the pieces of a group: steps of cost k from gs on, cut at multiples of width
+        auto pieces = [&](int64_t gs, int k, int blocks, bool alt, int group, int tile, int tile_rows, int row, int64_t area,
+                          int64_t stats) {
+            if (blocks == 0) return;
+            for (int c = (int)(gs / width); c < ctas; ++c) {
+                const int64_t s0 = max(ceil_div((int64_t)c * width - gs, k), (int64_t)0);
+                const int64_t s1 = min(ceil_div((int64_t)(c + 1) * width - gs, k), (int64_t)blocks);
+                if (s0 >= blocks) break;
+                if (s1 <= s0) continue;
+                for (int i = alt ? 0 : tile; i < (alt ? (s1 - s0 > 1 ? 2 : 1) : tile + 1); ++i) {
+                    const int64_t at = ((int64_t)(group + c) * 2 + i) * tile_rows + row;
+                    add(ws + area + at * D, reinterpret_cast<const float2*>(ws + stats)[at]);
+                }
+            }
+        };
+        if (plan.blocks > 0) {
+            const int pt = b / plan.group, q = b - pt * plan.group;
+            const int nreq = min(plan.group, a.B - pt * plan.group);
+            const bool alt = HILO || nreq <= TOK;
+            int k;
+            const int64_t gs = prefix_start(a, plan, pt, kh, &k);
+            const int tile = alt ? 0 : q / TOK;
+            pieces(gs, k, plan.blocks, alt, pt * a.Nkv + kh, tile, plan.tile_rows, (q - tile * TOK) * a.G + g, 0,
+                   plan.stats_area);
+        }
+        pieces(pre_cost + ((int64_t)s_before * a.Nkv + (int64_t)kh * nb) * plan.cost_own, plan.cost_own, nb, true,
+               b * a.Nkv + kh, 0, a.G, g, plan.own_area, plan.own_stats);
+        const bool any = M != -INFINITY;
+        const float inv = any ? __frcp_rn(L) : 0.0f;
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            const int d = lane + 32 * e;
+            float v = any ? __fmul_rn(acc[e], inv) : 0.0f;
+            if (C == ATT_I8 && any) {
+                if (a.offset_v) v = __fsub_rn(v, __ldg(a.offset_v + kh * D + d));
+                v = __fmul_rn(v, __ldg(a.scale_v + kh * D + d));
+            }
+            att_store<T>(a.out.base, (int64_t)b * a.out.tok + h * a.out.head + d, v);
+        }
+        if (a.lse && lane == 0) a.lse[(int64_t)b * a.Nq + h] = any ? __fmul_rn(__fadd_rn(M, log2f(L)), ATT_LN2) : -INFINITY;
+    }
+}
+
+}  // namespace kvq

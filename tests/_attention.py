@@ -8,13 +8,15 @@ import torch
 U = {torch.bfloat16: 2.0 ** -8, torch.float16: 2.0 ** -11}       # half a rounding step, relative
 
 
-def attend64(q, k, v, see, scale, u_out, u_p, kmag=None, vmag=None):
+def attend64(q, k, v, see, scale, u_out, u_p, kmag=None, vmag=None, u_q=0.0):
     """One head: rows q [n, D] over keys k [m, D], v [m, D] (float64); row i sees the keys that see[i] marks.
     Returns (out, lse, the bound of |out|'s error, the bound of lse's error).
 
     The bounds count, for a kernel with exact products and fp32 sums:
       ds    the scores: D + 8 roundings (2^-23 each, of the running sum) of sum |q| |k|, and of the score itself
-            when it is scaled, shifted by the maximum and exponentiated (2^-22 each of its magnitude);
+            when it is scaled, shifted by the maximum and exponentiated (2^-22 each of its magnitude); over int8
+            codes also u_q of sum |q| |k|, the rounding of q times the key scale (plus, for each channel, half a
+            subnormal f16 step, 2^-25 of the row's largest, which D of them bring to less than 2^-17 of it);
       sums  each of the m terms of the weights' sum and of the product with v: 2^-23 of the sum of magnitudes;
       u_p   the weights' rounding for the product with v (and, where they are f16, 2^-33 of the largest |v| for each
             key: half a subnormal step of weights that the kernels scale up by 2^8);
@@ -39,6 +41,9 @@ def attend64(q, k, v, see, scale, u_out, u_p, kmag=None, vmag=None):
     zero = s.new_zeros(n)
     ds = (q.shape[1] + 8) * 2.0 ** -23 * (mag.max(1).values if m else zero) + \
         2.0 ** -21 * (1 + (smax.max(1).values if m else zero))
+    if u_q:
+        big = (q.abs().max(1).values if n else zero) * (kmag.max() if m else 0.0) * abs(scale)
+        ds = ds + u_q * (mag.max(1).values if m else zero) + 2.0 ** -25 * q.shape[1] * big
     sums = (m + 64) * 2.0 ** -23
     a = w @ vm
     sub = m * 2.0 ** -33 * (vm.max() if m else 0.0) if u_p < 2.0 ** -9 else 0.0
@@ -101,6 +106,7 @@ def shared64(q, kc, vc, table, lens, prefix_table, prefix_len, scale_k=None, sca
     scale = D ** -0.5 if scale is None else scale
     u_out = U[q.dtype]
     u_p = U[torch.float16] if kc.dtype == torch.int8 else U[kc.dtype]
+    u_q = 0.0 if kc.dtype != torch.int8 else 2.0 ** -11 if q.dtype == torch.bfloat16 else 2.0 ** -22
     out = torch.full((B, Nq, D), math.nan, dtype=torch.float64, device=q.device)
     bound, lse, lb = out.clone(), out[..., 0].clone(), out[..., 0].clone()
     block = kc.shape[1]
@@ -117,7 +123,7 @@ def shared64(q, kc, vc, table, lens, prefix_table, prefix_len, scale_k=None, sca
             rows = slice(h * G, (h + 1) * G)
             see = torch.ones((G, k.shape[0]), dtype=torch.bool, device=q.device)
             out[b, rows], lse[b, rows], bound[b, rows], lb[b, rows] = attend64(q[b, rows].double(), k, v, see, scale, u_out,
-                                                                              u_p, km, vm)
+                                                                              u_p, km, vm, u_q)
     return out, lse, bound, lb
 
 
