@@ -342,12 +342,13 @@ KVQ_API kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k
 /* page mode (int8), or 16-bit caches of the same shape.                      */
 /*                                                                           */
 /* q, out   bf16 or f16 [B, Nq, D]; D = 64 or 128, strides as above.          */
-/* k_cache, v_cache   [num_pages, block, Nkv, D], int8 or q's type; only the  */
-/*          page dimension strided (a multiple of 16 bytes), 16-byte aligned. */
+/* k_cache, v_cache   [num_pages, block, Nkv, D], int8 or q's type, 16-byte   */
+/*          aligned; only the page dimension strided, alike in both and a     */
+/*          multiple of 64 bytes, less than 256 GB in all.                     */
 /* scale_k, scale_v   f32, Nkv*D elements, required for int8 caches:          */
 /* offset_k, offset_v value = (code - offset) * scale; offsets optional;      */
-/*          scale_k and offset_k 16-byte aligned.  NULL (else KVQ_ERR_ATTR)   */
-/*          for 16-bit caches.                                                 */
+/*          scale_k 16-byte aligned.  NULL (else KVQ_ERR_ATTR) for 16-bit     */
+/*          caches.                                                            */
 /* block_table   int32 [B, cols], columns contiguous, any row stride (0 too): */
 /*          the pages of each request's own tokens, which follow the prefix.  */
 /* seq_lens int32 [B]: own tokens of each request, 0 .. cols * block; -1: the */

@@ -129,7 +129,9 @@ kvq_status run_shared(const SharedArgs& a, cudaStream_t s) {
     constexpr uint32_t smem = sa_smem_bytes(D, I8);
     const int64_t ctas = persistent_grid(kernel, SA_THREADS, steps < SA_MAX_CTAS ? steps : SA_MAX_CTAS, smem);
     if (steps > 0 && launch(kernel, (unsigned)ctas, SA_THREADS, smem, s, mq, mq1, a, p) != cudaSuccess) return KVQ_ERR_CUDA;
-    return launched(launch(shared_join_kernel<T, C, D>, (unsigned)a.B, SJ_THREADS, 0, s, a, p, (int)ctas));
+    const int hblocks = (a.Nq + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
+    return launched(launch(shared_join_kernel<T, C, D>, (unsigned)(a.B * hblocks), SJ_THREADS, 0, s, a, p, (int)ctas,
+                           hblocks));
 }
 
 }  // namespace
@@ -251,9 +253,12 @@ kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_
     for (const kvq_tensor* c : {k_cache, v_cache}) {
         if (numel(c) == 0) continue;
         if (c->stride[3] != 1 || (Nkv > 1 && c->stride[2] != D) || (block > 1 && c->stride[1] != Nkv * D) ||
-            (pages > 1 && (c->stride[0] < block * Nkv * D || c->stride[0] * eb % 16 != 0)))
+            (pages > 1 && (c->stride[0] < block * Nkv * D || c->stride[0] * eb % 64 != 0 ||
+                           c->stride[0] != k_cache->stride[0])))
             return KVQ_ERR_LAYOUT;
     }
+    if (pages > 0 && pages * (pages > 1 ? k_cache->stride[0] : block * Nkv * D) * eb / 64 >= 0xFFFFFFFFll)
+        return KVQ_ERR_SHAPE;                                    // 256 GB: places are 32-bit units of 64 bytes
     const bool i8 = ctype == ATT_I8;
     const kvq_tensor* par[4] = {scale_k, scale_v, offset_k, offset_v};
     const float* pp[4] = {nullptr, nullptr, nullptr, nullptr};
@@ -311,12 +316,11 @@ kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_
     for (int i = 0; i < 4; ++i)
         if (par[i] && !pp[i]) return KVQ_ERR_NULL;
     if (!aligned16(q->data) || !aligned16(out->data) || !aligned16(k_cache->data) || !aligned16(v_cache->data) ||
-        !aligned16(pp[0]) || !aligned16(pp[2]) || !aligned16(a.workspace))
+        !aligned16(pp[0]) || !aligned16(a.workspace))
         return KVQ_ERR_LAYOUT;
     a.k_cache = static_cast<const uint8_t*>(k_cache->data);
     a.v_cache = static_cast<const uint8_t*>(v_cache->data);
-    a.k_page = (pages > 1 ? k_cache->stride[0] : 0) * eb;
-    a.v_page = (pages > 1 ? v_cache->stride[0] : 0) * eb;
+    a.page_bytes = (pages > 1 ? k_cache->stride[0] : 0) * eb;
     a.num_pages = pages;
     a.block = (int32_t)block;
     a.block_shift = -1;

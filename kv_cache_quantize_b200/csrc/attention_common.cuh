@@ -76,7 +76,7 @@ struct SharedArgs {
     float* lse;                    // [B, Nq] or null
     const uint8_t* k_cache;        // [pages, block, Nkv, D]
     const uint8_t* v_cache;
-    int64_t k_page, v_page;        // page strides in bytes
+    int64_t page_bytes;            // from page to page, a multiple of 64
     int64_t num_pages;
     int32_t block;                 // tokens per page
     int32_t block_shift;           // log2(block) when a power of two, else -1
@@ -130,6 +130,18 @@ __device__ __forceinline__ uint32_t pack2(float lo, float hi) {
     if (T == ATT_BF16) asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     else asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
+}
+
+template <int T>
+__device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
+    if (T == ATT_BF16) {
+        lo = __uint_as_float(w << 16);
+        hi = __uint_as_float(w & 0xFFFF0000u);
+    } else {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&w));
+        lo = f.x;
+        hi = f.y;
+    }
 }
 
 __device__ __forceinline__ float max3(float a, float b, float c) {

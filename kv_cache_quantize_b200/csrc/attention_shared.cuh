@@ -24,7 +24,9 @@
 //                    page lists, any page size; int8 codes are turned into f16
 //                    (exactly) on their way into the product's tiles;
 //   warp 12          one lane issues tcgen05.mma;
-//   warp 13          cuts the work, and loads Q where it needs no scaling.
+//   warp 13          cuts the work, and loads Q where it needs no scaling;
+//   warps 14, 15     scale Q over int8 caches, tile 0 and 1, for the next piece
+//                    while the tiles' last steps run.
 //
 // int8 caches: value = (code - offset) * scale per channel.  q is multiplied
 // by the key scale in fp32, scaled by a power of two per row to f16's range
@@ -43,7 +45,8 @@ constexpr int SA_THREADS = 512;
 constexpr int SA_KEYS = 128;
 constexpr int SA_ITEMS = 3;
 constexpr int SA_MAX_CTAS = 148;
-constexpr int SA_BAD = 8;                          // blocks whose missing keys are remembered
+constexpr int SA_BAD = 8;                          // steps whose missing keys are remembered
+constexpr int SA_PAGES = 3;                        // steps whose page numbers are kept
 constexpr float SA_SLACK = 7.0f;
 constexpr uint64_t SA_WAIT_NS = 2000000000ull;
 
@@ -54,7 +57,7 @@ __host__ __device__ constexpr int sa_lag(bool i8) { return i8 ? 3 : 2; }
 __host__ __device__ constexpr uint32_t sa_tile_bytes(int D) { return 128u * (uint32_t)D * 2u; }
 __host__ __device__ constexpr uint32_t sa_smem_bytes(int D, bool i8) {
     return (2u + (uint32_t)sa_ring(i8)) * sa_tile_bytes(D) + (i8 ? (uint32_t)(sa_lag(i8) + 1) * sa_tile_bytes(D) / 2u : 0u) +
-           512u + SA_BAD * 128u + 1024u;           // + barriers and items, key flags, alignment
+           512u + SA_PAGES * 512u + 512u;          // + barriers and items, page numbers, exponents
 }
 
 // the cost of a step: two tiles of rows, one tile (prefix), a request's own
@@ -138,14 +141,14 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     constexpr int NS = sa_ring(I8), LAG = sa_lag(I8), NR = LAG + 1;
     constexpr int PANELS = D / 64;
     constexpr uint32_t TILE = sa_tile_bytes(D), PANEL = 128 * 128, O_COL = 256;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    extern __shared__ __align__(1024) uint8_t smem[];        // no room for slack: the swizzle needs the alignment
     uint8_t* q_s = smem;
     uint8_t* kv_s = smem + 2 * TILE;
     uint8_t* raw_s = smem + (2 + NS) * TILE;
     uint8_t* after = raw_s + (I8 ? NR * (TILE / 2) : 0);
-    uint8_t* key_ok = after;                                 // [SA_BAD][128]
-    uint64_t* q_full = reinterpret_cast<uint64_t*>(after + SA_BAD * 128);
+    volatile uint32_t* row_at = reinterpret_cast<volatile uint32_t*>(after);             // [SA_PAGES][128]
+    volatile uint8_t* q_exp = after + SA_PAGES * 512;                                    // [2][2][128]
+    uint64_t* q_full = reinterpret_cast<uint64_t*>(after + SA_PAGES * 512 + 512);
     uint64_t* q_empty = q_full + 2;
     uint64_t* s_full = q_empty + 2;
     uint64_t* p_ready = s_full + 2;
@@ -154,17 +157,23 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     uint64_t* item_empty = item_full + SA_ITEMS;
     uint64_t* kv_full = item_empty + SA_ITEMS;
     uint64_t* kv_empty = kv_full + NS;
-    uint64_t* drain = kv_empty + NS;
+    uint64_t* page_bar = kv_empty + NS;
+    uint64_t* drain = page_bar + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);      // [SA_BAD]
-    volatile SharedItem* items = reinterpret_cast<volatile SharedItem*>(tmem_slot + 2 + SA_BAD);
+    volatile uint32_t* key_ok = bad + SA_BAD;                                          // [SA_BAD][4]: a bit per key
+    volatile SharedItem* items = reinterpret_cast<volatile SharedItem*>(tmem_slot + 2 + SA_BAD + 4 * SA_BAD);
     int* s_blocks = reinterpret_cast<int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int TOK = 128 / a.G;
 
+    if (smem_u32(smem) & 1023u) {                            // uniform over the grid; never on this hardware
+        if (threadIdx.x == 0) raise_fault(FAULT_TIMEOUT);
+        return;
+    }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], I8 ? 128 : 1);
+            mbar_init(&q_full[i], I8 ? 32 : 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 128);
@@ -172,12 +181,13 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         }
         for (int i = 0; i < SA_ITEMS; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], 13);                   // 8 softmax and 4 load warps, the MMA lane
+            mbar_init(&item_empty[i], HILO ? 14 : I8 ? 15 : 13);      // 8 softmax, 4 load and 0 to 2 Q warps, the MMA lane
         }
         for (int i = 0; i < NS; ++i) {
             mbar_init(&kv_full[i], 128);
             mbar_init(&kv_empty[i], 1);
         }
+        mbar_init(page_bar, 128);
         mbar_init(drain, 1);
         mbar_init_fence();
         *s_blocks = 0;
@@ -398,6 +408,88 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         }
     } else if (warp >= 14) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        // ---------------- Q times the key scale ----------------
+        if (I8 && !(HILO && warp == 15)) {
+            constexpr int LPR = D / 16;                      // lanes of a row, 16 channels each
+            constexpr int RPP = 32 / LPR;                    // rows of a pass
+            const int i = warp - 14;
+            const int sub = lane % LPR, c16 = sub * 16;
+            uint32_t used = 0;
+            for (uint32_t n_item = 0;; ++n_item) {
+                const uint32_t slot = n_item % SA_ITEMS;
+                if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
+                const int steps = items[slot].steps, alt = items[slot].alt, own = items[slot].own;
+                const int nreq = items[slot].nreq, kh = items[slot].kh;
+                const int b0 = items[slot].b0 + (alt ? 0 : i * TOK);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&item_empty[slot]);
+                if (steps < 0) break;
+                if (i && alt && steps == 1) continue;
+                if (!__all_sync(FULL_MASK, mbar_wait_ns(&q_empty[i], (used & 1u) ^ 1u, SA_WAIT_NS))) break;
+                const int rows = (alt ? nreq : min(nreq - i * TOK, TOK)) * a.G;
+                const int r_at = own && i && !HILO && a.G <= 96 ? 32 : 0;
+                float sc[16];
+                const float4* sk = reinterpret_cast<const float4*>(a.scale_k + kh * D + c16);
+#pragma unroll
+                for (int z = 0; z < 4; ++z) {
+                    const float4 e = __ldg(sk + z);
+                    sc[4 * z] = e.x;
+                    sc[4 * z + 1] = e.y;
+                    sc[4 * z + 2] = e.z;
+                    sc[4 * z + 3] = e.w;
+                }
+#pragma unroll 2
+                for (int r0 = 0; r0 < rows; r0 += RPP) {
+                    const int lr = r0 + lane / LPR;
+                    const bool live = lr < rows;
+                    const int b = b0 + (own || !live ? 0 : lr / a.G), h = kh * a.G + (!live ? 0 : own ? lr : lr % a.G);
+                    const uint4* q = reinterpret_cast<const uint4*>(a.q.base + ((int64_t)b * a.q.tok + h * a.q.head + c16) * 2);
+                    const uint4 e0 = __ldg(q), e1 = __ldg(q + 1);
+                    const uint32_t ew[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
+                    float x[16], top = 0.0f;
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) {
+                        float lo, hi;
+                        unpack2<T>(ew[z], lo, hi);
+                        x[2 * z] = __fmul_rn(lo, sc[2 * z]);
+                        x[2 * z + 1] = __fmul_rn(hi, sc[2 * z + 1]);
+                        top = fmaxf(top, fmaxf(fabsf(x[2 * z]), fabsf(x[2 * z + 1])));
+                    }
+#pragma unroll
+                    for (int d = 1; d < LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
+                    // the power of two below the row's largest; 127 (times one) where there is none
+                    uint32_t ex = __float_as_uint(top) >> 23;
+                    if (ex == 0 || ex >= 254) ex = 127;
+                    const float down = __uint_as_float((254u - ex) << 23);
+                    if (live) {
+                        const int r = r_at + lr;
+                        if (sub == 0) q_exp[((used & 1u) * 2 + i) * 128 + r] = (uint8_t)ex;
+                        uint32_t hi[8], lo[8];
+#pragma unroll
+                        for (int z = 0; z < 8; ++z) {
+                            const float a0 = __fmul_rn(x[2 * z], down), a1 = __fmul_rn(x[2 * z + 1], down);
+                            hi[z] = pack2<ATT_F16>(a0, a1);
+                            if (HILO) {
+                                float h0, h1;
+                                unpack2<ATT_F16>(hi[z], h0, h1);
+                                lo[z] = pack2<ATT_F16>(__fsub_rn(a0, h0), __fsub_rn(a1, h1));
+                            }
+                        }
+                        uint8_t* row = q_s + (HILO ? 0 : i) * TILE + (sub / 4) * PANEL + r * 128;
+                        const int p0 = ((2 * (sub & 3)) ^ (r & 7)) << 4, p1 = ((2 * (sub & 3) + 1) ^ (r & 7)) << 4;
+                        *reinterpret_cast<uint4*>(row + p0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(row + p1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                        if (HILO) {
+                            *reinterpret_cast<uint4*>(row + TILE + p0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            *reinterpret_cast<uint4*>(row + TILE + p1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                        }
+                    }
+                }
+                ++used;
+                fence_proxy_async_smem();
+                mbar_arrive(&q_full[i]);
+            }
+        }
     } else if (warp >= 8) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 120;");
         // ---------------- keys and values ----------------
@@ -407,7 +499,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         constexpr int RP = 128 / CH;                         // rows of a pass
         constexpr int PASSES = 128 / RP;
         const int ch = p % CH, r0 = p / CH;
-        const int64_t row_bytes = (int64_t)a.Nkv * D * EB;
+        const uint32_t row_units = (uint32_t)(a.Nkv * (D * EB / 64)), page_units = (uint32_t)(a.page_bytes / 64);
         uint32_t issued = 0, done = 0, block_no = 0;
         bool ok = true;
         auto finish = [&]() {
@@ -419,9 +511,12 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 uint8_t* dst = kv_s + (done % NS) * TILE + (ch / 4) * PANEL;
                 const int c0 = 2 * (ch & 3);
                 const int first = (ch >> 2) & 1;             // panel 1 starts with the other half: no bank conflict
+                uint4 raw[PASSES];
+#pragma unroll
+                for (int k = 0; k < PASSES; ++k) raw[k] = *reinterpret_cast<const uint4*>(src + k * 2048);
 #pragma unroll
                 for (int k = 0; k < PASSES; ++k) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(src + k * 2048);
+                    const uint4 w = raw[k];
                     const int r = r0 + k * RP;
                     uint4 h[2];
                     i8x4_f16(w.x, h[0].x, h[0].y);
@@ -448,6 +543,19 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             if (n < 0) break;
             const int32_t* list = own ? a.table + (int64_t)b0 * a.table_stride : a.prefix_table;
             const int64_t head = (int64_t)kh * D * EB + ch * 16;
+            // thread p looks up the place of key p of each step, one step ahead, in units of 64 bytes from the
+            // cache's start (a token's values are a multiple of that)
+            auto lookup = [&](int s) {
+                const int t = s * SA_KEYS + p;
+                if (t >= keys) return 0xFFFFFFFFu;
+                const uint32_t tok = (uint32_t)(key0 + t);
+                const uint32_t e = a.block_shift >= 0 ? tok >> a.block_shift : tok / (uint32_t)a.block;
+                const int32_t page = __ldg(list + e);
+                const uint32_t in = (tok - e * (uint32_t)a.block) * row_units;
+                return (uint32_t)page < (uint32_t)a.num_pages ? (uint32_t)page * page_units + in : 0xFFFFFFFFu;
+            };
+            const uint32_t block0 = block_no;
+            uint32_t next = lookup(0);
             for (int q = 0; q < 2 * n && ok; ++q) {
                 // the order K0 K1 V0 K2 V1 ... V(n-1)
                 const bool is_v = q > 0 && ((q & 1) == 0 || q == 2 * n - 1);
@@ -456,34 +564,35 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                     ok = __all_sync(FULL_MASK, mbar_wait_ns(&kv_empty[issued % NS], ((issued / NS) & 1u) ^ 1u, SA_WAIT_NS));
                     if (!ok) break;
                 }
+                volatile uint32_t* place = row_at + ((block0 + s) % SA_PAGES) * 128;
+                if (!is_v) {
+                    const bool there = next != 0xFFFFFFFFu;
+                    place[p] = next;
+                    const unsigned word = __ballot_sync(FULL_MASK, there);
+                    if (lane == 0) key_ok[(block_no % SA_BAD) * 4 + (p >> 5)] = word;
+                    if (!there && s * SA_KEYS + p < keys) {
+                        bad[block_no % SA_BAD] = block_no + 1;
+                        raise_fault(FAULT_SLOT_RANGE);
+                    }
+                    ++block_no;
+                    mbar_arrive(page_bar);
+                    ok = __all_sync(FULL_MASK, mbar_wait_ns(page_bar, (block_no & 1u) ^ 1u, SA_WAIT_NS));
+                    if (!ok) break;
+                    if (s + 1 < n) next = lookup(s + 1);
+                }
                 const uint8_t* base = (is_v ? a.v_cache : a.k_cache) + head;
-                const int64_t page_bytes = is_v ? a.v_page : a.k_page;
                 const uint32_t dst = I8 ? smem_u32(raw_s + (issued % NR) * (TILE / 2) + p * 16)
                                         : smem_u32(kv_s + (issued % NS) * TILE + (ch / 8) * PANEL);
-                const uint32_t nb = block_no % SA_BAD;
+                uint32_t at[PASSES];
+#pragma unroll
+                for (int k = 0; k < PASSES; ++k) at[k] = place[r0 + k * RP];
 #pragma unroll
                 for (int k = 0; k < PASSES; ++k) {
                     const int r = r0 + k * RP;
-                    const int t = s * SA_KEYS + r;           // key of the piece
-                    const uint8_t* src = base;
-                    uint32_t bytes = 0;
-                    if (t < keys) {
-                        const int32_t tok = key0 + t;
-                        const int32_t e = a.block_shift >= 0 ? tok >> a.block_shift : tok / a.block;
-                        const int32_t page = __ldg(list + e);
-                        if ((uint32_t)page < (uint32_t)a.num_pages) {
-                            src = base + page * page_bytes + (tok - e * a.block) * row_bytes;
-                            bytes = 16;
-                        }
-                        if (!is_v && ch == 0) key_ok[nb * 128 + r] = bytes != 0;
-                        if (!is_v && bytes == 0) {
-                            bad[nb] = block_no + 1;
-                            raise_fault(FAULT_SLOT_RANGE);
-                        }
-                    }
-                    cp_async16(I8 ? dst + k * 2048 : dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4), src, bytes);
+                    const bool there = at[k] != 0xFFFFFFFFu;
+                    cp_async16(I8 ? dst + k * 2048 : dst + r * 128 + (((ch & 7) ^ (r & 7)) << 4),
+                               base + (there ? (uint64_t)at[k] * 64u : 0u), there ? 16u : 0u);
                 }
-                if (!is_v) ++block_no;
                 cp_async_commit();
                 ++issued;
                 if (issued - done > LAG) {
@@ -528,118 +637,50 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             const int lr = w.own && i && !HILO && a.G <= 96 ? r - 32 : r;
             const bool live = lr >= 0 && lr < rows;
             const bool work = __any_sync(FULL_MASK, live);
-            float c = c0, koff = 0.0f;
-            if (I8 && first < w.steps) {
-                if (HILO && i == 0) {
-                    // both tiles read these rows: the earlier item's products are done with them
-                    ok = __all_sync(FULL_MASK, mbar_wait_ns(&q_empty[0], (q_n++ & 1u) ^ 1u, SA_WAIT_NS));
-                    if (!ok) break;
-                }
-                if (live) {
-                    const int b = w.b0 + (w.alt ? 0 : i * TOK) + (w.own ? 0 : lr / a.G);
-                    const int h = w.kh * a.G + (w.own ? lr : lr % a.G);
-                    const uint4* q = reinterpret_cast<const uint4*>(a.q.base + ((int64_t)b * a.q.tok + h * a.q.head) * 2);
-                    const float4* sk = reinterpret_cast<const float4*>(a.scale_k + w.kh * D);
-                    const float4* ok4 = reinterpret_cast<const float4*>(a.offset_k + w.kh * D);
-                    auto scaled = [&](int k, float (&x)[8]) {
-                        const uint4 e = __ldg(q + k);
-                        const float4 u = __ldg(sk + 2 * k), v = __ldg(sk + 2 * k + 1);
-                        const uint32_t ew[4] = {e.x, e.y, e.z, e.w};
-                        const float sc[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int z = 0; z < 8; ++z)
-                            x[z] = __fmul_rn(att_load<T>(reinterpret_cast<const uint8_t*>(ew), z), sc[z]);
-                    };
-                    float top = 0.0f;
-#pragma unroll 4
-                    for (int k = 0; k < D / 8; ++k) {
-                        float x[8];
-                        scaled(k, x);
-#pragma unroll
-                        for (int z = 0; z < 8; ++z) top = fmaxf(top, fabsf(x[z]));
-                    }
-                    const uint32_t ex = __float_as_uint(top) >> 23;                  // power of two below the maximum
-                    const bool norm = ex > 0 && ex < 254;
-                    const float down = norm ? __uint_as_float((254u - ex) << 23) : 1.0f;
-                    c = norm ? fmaxf(__fmul_rn(c0, __uint_as_float(ex << 23)), 1.17549435e-38f) : c0;
-                    const bool store = !HILO || i == 0;
-                    const bool sum = a.lse != nullptr && a.offset_k != nullptr;
-#pragma unroll 2
-                    for (int k = 0; k < D / 8; ++k) {
-                        float x[8];
-                        scaled(k, x);
-                        uint32_t hi[4], lo[4];
-                        const float4 u = sum ? __ldg(ok4 + 2 * k) : float4{}, v = sum ? __ldg(ok4 + 2 * k + 1) : float4{};
-                        const float of[8] = {u.x, u.y, u.z, u.w, v.x, v.y, v.z, v.w};
-#pragma unroll
-                        for (int z = 0; z < 4; ++z) {
-                            const float a0 = __fmul_rn(x[2 * z], down), a1 = __fmul_rn(x[2 * z + 1], down);
-                            hi[z] = pack2<ATT_F16>(a0, a1);
-                            float h0 = __half2float(__ushort_as_half((unsigned short)(hi[z] & 0xFFFFu)));
-                            float h1 = __half2float(__ushort_as_half((unsigned short)(hi[z] >> 16)));
-                            if (HILO) {
-                                lo[z] = pack2<ATT_F16>(__fsub_rn(a0, h0), __fsub_rn(a1, h1));
-                                h0 = __fadd_rn(h0, __half2float(__ushort_as_half((unsigned short)(lo[z] & 0xFFFFu))));
-                                h1 = __fadd_rn(h1, __half2float(__ushort_as_half((unsigned short)(lo[z] >> 16))));
-                            }
-                            koff = __fmaf_rn(h0, of[2 * z], koff);
-                            koff = __fmaf_rn(h1, of[2 * z + 1], koff);
-                        }
-                        if (store) {
-                            const uint32_t off = (k / 8) * PANEL + r * 128 + (((k & 7) ^ (r & 7)) << 4);
-                            *reinterpret_cast<uint4*>(q_s + (HILO ? 0 : i) * TILE + off) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            if (HILO) *reinterpret_cast<uint4*>(q_s + TILE + off) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                        }
-                    }
-                    if (flip) koff = -koff;
-                }
-                if (!HILO || i == 0) {
-                    fence_proxy_async_smem();
-                    mbar_arrive(&q_full[i]);
-                }
-            }
+            float c = c0;
             float m = -INFINITY, l = 0.0f;
             for (int s = first; s < w.steps; s += stride) {
                 ok = __all_sync(FULL_MASK, mbar_wait_ns(&s_full[i], s_n++ & 1u, SA_WAIT_NS));
                 if (!ok) break;
                 tm_fence_after();
+                if (I8 && s == first) {
+                    // the row's power of two (Q of this piece is in place: S came from it)
+                    const uint32_t ex = q_exp[((q_n++ & 1u) * 2 + (HILO ? 0 : i)) * 128 + r];
+                    c = fmaxf(__fmul_rn(c0, __uint_as_float(ex << 23)), 1.17549435e-38f);
+                }
                 if (work) {
                     const int see = w.keys - s * SA_KEYS;
                     const uint32_t blk = block_no + s;
                     const bool gaps = bad[blk % SA_BAD] == blk + 1;
-                    // 64 scores at a time, read twice: once for the maximum, once for the weights
-                    auto load = [&](int half, uint32_t (&x)[64]) {
+                    if (flip | (see < SA_KEYS) | gaps) {
+                        // the uncommon cases are put right in TMEM, to keep the common code short:
+                        // a negative scale, keys that are not there
+#pragma unroll 1
+                        for (int k0 = 0; k0 < SA_KEYS; k0 += 32) {
+                            uint32_t have = see - k0 >= 32 ? 0xFFFFFFFFu : see > k0 ? (1u << (see - k0)) - 1u : 0u;
+                            if (gaps) have &= key_ok[(blk % SA_BAD) * 4 + k0 / 32];
+                            uint32_t x[32];
+                            tm_ld32(s_t + k0, x);
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) x[k] = (have >> k) & 1u ? x[k] ^ flip : 0xFF800000u;
+                            tm_st32(s_t + k0, x);
+                        }
+                        tm_wait_st();
+                    }
+                    // the scores are read twice, 64 at a time: for the maximum and for the weights
+                    float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll 1
+                    for (int half = 0; half < 2; ++half) {
+                        uint32_t x[64];
                         tm_ld64(s_t + 64 * half, x);
-                        if (flip) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k) x[k] ^= flip;
-                        }
-                        if (see < 64 * half + 64) {
-#pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (64 * half + k >= see) x[k] = 0xFF800000u;
-                        }
-                        if (gaps) {
-                            const uint8_t* have = key_ok + (blk % SA_BAD) * 128 + 64 * half;
-#pragma unroll
-                            for (int k = 0; k < 64; ++k)
-                                if (!have[k]) x[k] = 0xFF800000u;
-                        }
-                    };
-                    float bm = -INFINITY;
-                    uint32_t x[64];
-#pragma unroll
-                    for (int half = 1; half >= 0; --half) {
-                        load(half, x);
-                        float mx[4] = {bm, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
                         for (int k = 0; k < 64; k += 8) {
 #pragma unroll
                             for (int q = 0; q < 4; ++q)
                                 mx[q] = max3(mx[q], __uint_as_float(x[k + 2 * q]), __uint_as_float(x[k + 2 * q + 1]));
                         }
-                        bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                     }
+                    const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                     const bool grow = __fmul_rn(__fsub_rn(bm, m), c) > SA_SLACK || (m == -INFINITY && bm > m);
                     if (s == first) {
                         m = bm;
@@ -659,9 +700,11 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                     const float ms = m == -INFINITY ? 0.0f : __fmaf_rn(m, c, -SHIFT);
                     const uint64_t c2 = f32x2(c, c), ms2 = f32x2(-ms, -ms);
                     uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
+#pragma unroll 1
                     for (int half = 0; half < 2; ++half) {
-                        if (half) load(1, x);                 // half 0 is still here; its weights go over scores read already
+                        // the weights go over scores that have been read: keys 0 .. 127 into columns 0 .. 63
+                        uint32_t x[64];
+                        tm_ld64(s_t + 64 * half, x);
 #pragma unroll
                         for (int g = 0; g < 2; ++g) {
                             uint32_t pk[16];
@@ -689,7 +732,10 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             }
             if (!ok) break;
             block_no += w.steps;
-            if (first >= w.steps) continue;
+            if (first >= w.steps) {
+                if (HILO) ++q_n;                              // the exponents count tile 0's pieces
+                continue;
+            }
             ok = __all_sync(FULL_MASK, mbar_wait_ns(&o_full[i], o_n++ & 1u, SA_WAIT_NS));
             if (!ok) break;
             tm_fence_after();
@@ -710,7 +756,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 if (live) {
                     float2* st = reinterpret_cast<float2*>(ws + (w.own ? plan.own_stats : plan.stats_area)) + row;
                     // a row of NaN scores has no maximum: its sum, NaN, must still count
-                    *st = make_float2(m == -INFINITY ? (l != l ? 0.0f : m) : __fsub_rn(__fmaf_rn(m, c, -SHIFT), __fmul_rn(koff, c)), l);
+                    *st = make_float2(m == -INFINITY ? (l != l ? 0.0f : m) : __fmaf_rn(m, c, -SHIFT), l);
                 }
             }
             tm_fence_before();
@@ -733,16 +779,19 @@ constexpr int SJ_THREADS = 256;
 
 template <int T, int C, int D>
 __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_constant__ SharedArgs a,
-                                                                const __grid_constant__ SharedPlan plan, int ctas) {
+                                                                const __grid_constant__ SharedPlan plan, int ctas,
+                                                                int hblocks) {
     constexpr bool HILO = C == ATT_I8 && T == ATT_F16;
     constexpr int E = D / 32;
     __shared__ int s_all, s_before;
+    __shared__ int64_t s_at[SJ_THREADS / 32][32];            // the pieces found: where and how much
+    __shared__ float s_w[SJ_THREADS / 32][32];
     const int lane = threadIdx.x & 31;
     if (threadIdx.x == 0) s_all = s_before = 0;
     __syncthreads();
     pdl_wait();
     pdl_trigger();
-    const int b = blockIdx.x;
+    const int b = blockIdx.x / hblocks;
     {
         int n = 0, before = 0;
         for (int k = threadIdx.x; k < a.B; k += SJ_THREADS) {
@@ -765,60 +814,114 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
     const int nb = own_blocks(a, b);
     const int TOK = 128 / a.G;
     const float* ws = reinterpret_cast<const float*>(a.workspace);
-    for (int h = threadIdx.x >> 5; h < a.Nq; h += SJ_THREADS / 32) {
-        const int kh = h / a.G, g = h - kh * a.G;
-        float M = -INFINITY, L = 0.0f, acc[E];
+    const int h = (int)(blockIdx.x % hblocks) * (SJ_THREADS / 32) + (threadIdx.x >> 5);
+    if (h >= a.Nq) return;
+    const int kh = h / a.G, g = h - kh * a.G;
+    const int warp = threadIdx.x >> 5;
+    float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-        auto add = [&](const float* o, float2 st) {
-            if (st.x == -INFINITY) return;
-            const float mn = fmaxf(M, st.x);
-            const float f = exp2f(__fsub_rn(M, mn)), w = exp2f(__fsub_rn(st.x, mn));
-            L = __fmaf_rn(L, f, __fmul_rn(st.y, w));
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(acc[e], f, __fmul_rn(o[lane + 32 * e], w));
-            M = mn;
-        };
-        // the pieces of a group: steps of cost k from gs on, cut at multiples of width
-        auto pieces = [&](int64_t gs, int k, int blocks, bool alt, int group, int tile, int tile_rows, int row, int64_t area,
-                          int64_t stats) {
-            if (blocks == 0) return;
-            for (int c = (int)(gs / width); c < ctas; ++c) {
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    // the pieces of a group: steps of cost k from gs on, cut at multiples of
+    // width; a lane finds one piece (CTA c, tile i), 32 at a time
+    auto pieces = [&](int64_t gs, int k, int blocks, bool alt, int group, int tile, int tile_rows, int row, int64_t area,
+                      int64_t stats) {
+        const int c0 = (int)(gs / width), c1 = (int)((gs + (int64_t)k * blocks - 1) / width);
+        const int per = alt ? 2 : 1;
+        for (int base = 0; base < (c1 - c0 + 1) * per; base += 32) {
+            const int c = c0 + (base + lane) / per, i = alt ? (base + lane) & 1 : tile;
+            float2 st = make_float2(-INFINITY, 0.0f);
+            int64_t at = 0;
+            if (c <= c1) {
                 const int64_t s0 = max(ceil_div((int64_t)c * width - gs, k), (int64_t)0);
                 const int64_t s1 = min(ceil_div((int64_t)(c + 1) * width - gs, k), (int64_t)blocks);
-                if (s0 >= blocks) break;
-                if (s1 <= s0) continue;
-                for (int i = alt ? 0 : tile; i < (alt ? (s1 - s0 > 1 ? 2 : 1) : tile + 1); ++i) {
-                    const int64_t at = ((int64_t)(group + c) * 2 + i) * tile_rows + row;
-                    add(ws + area + at * D, reinterpret_cast<const float2*>(ws + stats)[at]);
+                if (s1 - s0 > (alt ? i : 0)) {
+                    at = ((int64_t)(group + c) * 2 + i) * tile_rows + row;
+                    st = reinterpret_cast<const float2*>(ws + stats)[at];
                 }
             }
-        };
-        if (plan.blocks > 0) {
-            const int pt = b / plan.group, q = b - pt * plan.group;
-            const int nreq = min(plan.group, a.B - pt * plan.group);
-            const bool alt = HILO || nreq <= TOK;
-            int k;
-            const int64_t gs = prefix_start(a, plan, pt, kh, &k);
-            const int tile = alt ? 0 : q / TOK;
-            pieces(gs, k, plan.blocks, alt, pt * a.Nkv + kh, tile, plan.tile_rows, (q - tile * TOK) * a.G + g, 0,
-                   plan.stats_area);
+            float top = st.x;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
+            const float mn = fmaxf(M, top);
+            if (mn == -INFINITY) continue;                    // nothing visible so far
+            const float f = exp2f(__fsub_rn(M, mn));
+            const bool has = st.x != -INFINITY;
+            const float w = has ? exp2f(__fsub_rn(st.x, mn)) : 0.0f;
+            float sum = has ? __fmul_rn(st.y, w) : 0.0f;
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(FULL_MASK, sum, d));
+            L = __fmaf_rn(L, f, sum);
+            M = mn;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = __fmul_rn(acc[e], f);
+            const unsigned mask = __ballot_sync(FULL_MASK, has);
+            const int count = __popc(mask);
+            __syncwarp();
+            if (has) {
+                const int n = __popc(mask & ((1u << lane) - 1u));
+                s_at[warp][n] = area + at * D;
+                s_w[warp][n] = w;
+            }
+            __syncwarp();
+#pragma unroll 4
+            for (int n = 0; n < count; ++n) {
+                const float* o = ws + s_at[warp][n] + lane * E;
+                const float wn = s_w[warp][n];
+                float v[E];
+                if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
+                else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
+#pragma unroll
+                for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(v[e], wn, acc[e]);
+            }
         }
+    };
+    if (plan.blocks > 0) {
+        const int pt = b / plan.group, q = b - pt * plan.group;
+        const int nreq = min(plan.group, a.B - pt * plan.group);
+        const bool alt = HILO || nreq <= TOK;
+        int k;
+        const int64_t gs = prefix_start(a, plan, pt, kh, &k);
+        const int tile = alt ? 0 : q / TOK;
+        pieces(gs, k, plan.blocks, alt, pt * a.Nkv + kh, tile, plan.tile_rows, (q - tile * TOK) * a.G + g, 0,
+               plan.stats_area);
+    }
+    if (nb > 0)
         pieces(pre_cost + ((int64_t)s_before * a.Nkv + (int64_t)kh * nb) * plan.cost_own, plan.cost_own, nb, true,
                b * a.Nkv + kh, 0, a.G, g, plan.own_area, plan.own_stats);
-        const bool any = M != -INFINITY;
-        const float inv = any ? __frcp_rn(L) : 0.0f;
+    const bool any = M != -INFINITY;
+    const float inv = any ? __frcp_rn(L) : 0.0f;
+    const int d0 = lane * E;
+    uint32_t packed[E / 2];
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-            const int d = lane + 32 * e;
-            float v = any ? __fmul_rn(acc[e], inv) : 0.0f;
+    for (int e = 0; e < E; e += 2) {
+        float v[2];
+#pragma unroll
+        for (int z = 0; z < 2; ++z) {
+            v[z] = any ? __fmul_rn(acc[e + z], inv) : 0.0f;
             if (C == ATT_I8 && any) {
-                if (a.offset_v) v = __fsub_rn(v, __ldg(a.offset_v + kh * D + d));
-                v = __fmul_rn(v, __ldg(a.scale_v + kh * D + d));
+                if (a.offset_v) v[z] = __fsub_rn(v[z], __ldg(a.offset_v + kh * D + d0 + e + z));
+                v[z] = __fmul_rn(v[z], __ldg(a.scale_v + kh * D + d0 + e + z));
             }
-            att_store<T>(a.out.base, (int64_t)b * a.out.tok + h * a.out.head + d, v);
         }
-        if (a.lse && lane == 0) a.lse[(int64_t)b * a.Nq + h] = any ? __fmul_rn(__fadd_rn(M, log2f(L)), ATT_LN2) : -INFINITY;
+        packed[e / 2] = pack2<T>(v[0], v[1]);
+    }
+    uint8_t* out = a.out.base + ((int64_t)b * a.out.tok + h * a.out.head + d0) * 2;
+    if (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(packed[0], packed[E / 2 - 1]);
+    else *reinterpret_cast<uint32_t*>(out) = packed[0];
+    if (a.lse) {
+        // the key offset's share of every score of the row
+        float off = 0.0f;
+        if (C == ATT_I8 && a.offset_k) {
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                off = __fmaf_rn(__fmul_rn(att_load<T>(a.q.base, (int64_t)b * a.q.tok + h * a.q.head + d0 + e),
+                                          __ldg(a.scale_k + kh * D + d0 + e)), __ldg(a.offset_k + kh * D + d0 + e), off);
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) off = __fadd_rn(off, __shfl_xor_sync(FULL_MASK, off, d));
+        }
+        if (lane == 0)
+            a.lse[(int64_t)b * a.Nq + h] =
+                any ? __fsub_rn(__fmul_rn(__fadd_rn(M, log2f(L)), ATT_LN2), __fmul_rn(off, a.scale)) : -INFINITY;
     }
 }
 

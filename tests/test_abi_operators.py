@@ -118,7 +118,10 @@ def shared(L, **kw):
     ({"lse": t((8, 5), F32)}, ESHAPE),
     ({"q": t((5, 8, 32), BF), "out": t((5, 8, 32), BF)}, EUNSUP),
     ({"k": t((40, 16, 2, 128), I8, (4096, 256, 129, 1))}, ELAYOUT), ({"k": t((40, 16, 2, 128), I8, (4100, 256, 128, 1))}, ELAYOUT),
-    ({"v": t((40, 16, 2, 128), I8, (4095, 256, 128, 1))}, ELAYOUT), ({"table": t((5, 6), I32, (12, 2))}, ELAYOUT),
+    ({"v": t((40, 16, 2, 128), I8, (4095, 256, 128, 1))}, ELAYOUT),
+    ({"v": t((40, 16, 2, 128), I8, (4160, 256, 128, 1))}, ELAYOUT),
+    ({"k": t((40, 16, 2, 128), I8, (4112, 256, 128, 1)), "v": t((40, 16, 2, 128), I8, (4112, 256, 128, 1))}, ELAYOUT),
+    ({"k": t((1 << 27, 16, 2, 128), I8), "v": t((1 << 27, 16, 2, 128), I8)}, ESHAPE), ({"table": t((5, 6), I32, (12, 2))}, ELAYOUT),
     ({"lens": t((5,), I32, (2,))}, ELAYOUT), ({"out": t((5, 8, 128), BF, (0, 128, 1))}, ELAYOUT),
     ({"sk": t((2, 128), F32, (1, 2))}, ELAYOUT),
 ])

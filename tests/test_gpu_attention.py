@@ -303,6 +303,12 @@ def test_shared_batches(batch, dtype, cache):
 
 
 @pytest.mark.parametrize("dtype,cache", KINDS)
+def test_shared_many_requests(dtype, cache):
+    """More pieces of work than multiprocessors: every one of them takes several, of all kinds."""
+    run_shared(paged(34, [(i * 53) % 400 for i in range(150)], 700, 8, 4, 64, 16, dtype, cache))
+
+
+@pytest.mark.parametrize("dtype,cache", KINDS)
 def test_shared_long(dtype, cache):
     run_shared(paged(25, [3000, 20, 1500], 5000, 16, 4, 128, 64, dtype, cache))
     run_shared(paged(26, [9000], 0, 4, 1, 128, 64, dtype, cache))
