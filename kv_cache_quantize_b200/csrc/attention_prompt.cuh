@@ -234,22 +234,21 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             uint32_t pos = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0};
             auto wait_kv = [&](uint32_t k) { return mbar_wait_ns(&kv_full[k % NS], (k / NS) & 1u, PA_WAIT_NS); };
             auto scores = [&](int i, uint32_t k) {
-                const uint32_t qa = smem_u32(q_s + i * TILE), ka = smem_u32(kv_s + (k % NS) * TILE);
+                const uint64_t qd = umma_desc_k(smem_u32(q_s + i * TILE)), kd = umma_desc_k(smem_u32(kv_s + (k % NS) * TILE));
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
-                    const uint32_t off = (d / 4) * PANEL + (d % 4) * 32;
-                    umma_ss(tmem + 128 * i, umma_desc_k(qa + off), umma_desc_k(ka + off), ID_S, d != 0);
+                    const uint32_t off = ((d / 4) * PANEL + (d % 4) * 32) >> 4;
+                    umma_ss(tmem + 128 * i, qd + off, kd + off, ID_S, d != 0);
                 }
                 umma_done(&s_full[i]);
             };
             auto values = [&](int i, uint32_t k, bool first) {
-                const uint32_t va = smem_u32(kv_s + (k % NS) * TILE);
+                const uint64_t vd = umma_desc_mn(smem_u32(kv_s + (k % NS) * TILE), PANEL);
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < PA_KEYS / 16; ++d)
-                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, umma_desc_mn(va + 2048 * d, PANEL), ID_O,
-                            !first || d != 0);
+                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, vd + 128 * d, ID_O, !first || d != 0);
             };
             bool ok = true;
             for (uint32_t n_item = 0; ok; ++n_item) {

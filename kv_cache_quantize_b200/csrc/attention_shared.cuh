@@ -340,24 +340,23 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             uint32_t pos = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0};
             auto wait_kv = [&](uint32_t k) { return mbar_wait_ns(&kv_full[k % NS], (k / NS) & 1u, SA_WAIT_NS); };
             auto scores = [&](int i, uint32_t k) {
-                const uint32_t ka = smem_u32(kv_s + (k % NS) * TILE);
+                const uint64_t qd = umma_desc_k(smem_u32(q_s + (HILO ? 0 : i) * TILE));
+                const uint64_t kd = umma_desc_k(smem_u32(kv_s + (k % NS) * TILE));
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
-                    const uint32_t off = (d / 4) * PANEL + (d % 4) * 32;
-                    const uint64_t kd = umma_desc_k(ka + off);
-                    umma_ss(tmem + 128 * i, umma_desc_k(smem_u32(q_s + (HILO ? 0 : i) * TILE) + off), kd, ID_S, d != 0);
-                    if (HILO) umma_ss(tmem + 128 * i, umma_desc_k(smem_u32(q_s + TILE) + off), kd, ID_S, true);
+                    const uint32_t off = ((d / 4) * PANEL + (d % 4) * 32) >> 4;
+                    umma_ss(tmem + 128 * i, qd + off, kd + off, ID_S, d != 0);
+                    if (HILO) umma_ss(tmem + 128 * i, qd + (TILE >> 4) + off, kd + off, ID_S, true);
                 }
                 umma_done(&s_full[i]);
             };
             auto values = [&](int i, uint32_t k, bool first) {
-                const uint32_t va = smem_u32(kv_s + (k % NS) * TILE);
+                const uint64_t vd = umma_desc_mn(smem_u32(kv_s + (k % NS) * TILE), PANEL);
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < SA_KEYS / 16; ++d)
-                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, umma_desc_mn(va + 2048 * d, PANEL), ID_O,
-                            !first || d != 0);
+                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, vd + 128 * d, ID_O, !first || d != 0);
             };
             bool ok = true;
             for (uint32_t n_item = 0; ok; ++n_item) {
@@ -438,50 +437,62 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                     sc[4 * z + 2] = e.z;
                     sc[4 * z + 3] = e.w;
                 }
-#pragma unroll 2
-                for (int r0 = 0; r0 < rows; r0 += RPP) {
-                    const int lr = r0 + lane / LPR;
-                    const bool live = lr < rows;
-                    const int b = b0 + (own || !live ? 0 : lr / a.G), h = kh * a.G + (!live ? 0 : own ? lr : lr % a.G);
-                    const uint4* q = reinterpret_cast<const uint4*>(a.q.base + ((int64_t)b * a.q.tok + h * a.q.head + c16) * 2);
-                    const uint4 e0 = __ldg(q), e1 = __ldg(q + 1);
-                    const uint32_t ew[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
-                    float x[16], top = 0.0f;
+                uint4 e[4][2];
+#pragma unroll 1
+                for (int r0 = 0; r0 < rows; r0 += 4 * RPP) {
+                    // four passes' loads are in flight together
 #pragma unroll
-                    for (int z = 0; z < 8; ++z) {
-                        float lo, hi;
-                        unpack2<T>(ew[z], lo, hi);
-                        x[2 * z] = __fmul_rn(lo, sc[2 * z]);
-                        x[2 * z + 1] = __fmul_rn(hi, sc[2 * z + 1]);
-                        top = fmaxf(top, fmaxf(fabsf(x[2 * z]), fabsf(x[2 * z + 1])));
+                    for (int z = 0; z < 4; ++z) {
+                        const int lr = r0 + z * RPP + lane / LPR;
+                        const int b = b0 + (own ? 0 : lr / a.G), h = kh * a.G + (own ? lr : lr % a.G);
+                        const uint4* q = reinterpret_cast<const uint4*>(a.q.base + ((int64_t)b * a.q.tok + h * a.q.head + c16) * 2);
+                        e[z][0] = lr < rows ? __ldg(q) : make_uint4(0u, 0u, 0u, 0u);
+                        e[z][1] = lr < rows ? __ldg(q + 1) : make_uint4(0u, 0u, 0u, 0u);
                     }
 #pragma unroll
-                    for (int d = 1; d < LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
-                    // the power of two below the row's largest; 127 (times one) where there is none
-                    uint32_t ex = __float_as_uint(top) >> 23;
-                    if (ex == 0 || ex >= 254) ex = 127;
-                    const float down = __uint_as_float((254u - ex) << 23);
-                    if (live) {
-                        const int r = r_at + lr;
-                        if (sub == 0) q_exp[((used & 1u) * 2 + i) * 128 + r] = (uint8_t)ex;
-                        uint32_t hi[8], lo[8];
+                    for (int u = 0; u < 4; ++u) {
+                        if (r0 + u * RPP >= rows) break;
+                        const int lr = r0 + u * RPP + lane / LPR;
+                        const bool live = lr < rows;
+                        const uint4 e0 = e[u][0], e1 = e[u][1];
+                        const uint32_t ew[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
+                        float x[16], top = 0.0f;
 #pragma unroll
                         for (int z = 0; z < 8; ++z) {
-                            const float a0 = __fmul_rn(x[2 * z], down), a1 = __fmul_rn(x[2 * z + 1], down);
-                            hi[z] = pack2<ATT_F16>(a0, a1);
-                            if (HILO) {
-                                float h0, h1;
-                                unpack2<ATT_F16>(hi[z], h0, h1);
-                                lo[z] = pack2<ATT_F16>(__fsub_rn(a0, h0), __fsub_rn(a1, h1));
-                            }
+                            float lo, hi;
+                            unpack2<T>(ew[z], lo, hi);
+                            x[2 * z] = __fmul_rn(lo, sc[2 * z]);
+                            x[2 * z + 1] = __fmul_rn(hi, sc[2 * z + 1]);
+                            top = fmaxf(top, fmaxf(fabsf(x[2 * z]), fabsf(x[2 * z + 1])));
                         }
-                        uint8_t* row = q_s + (HILO ? 0 : i) * TILE + (sub / 4) * PANEL + r * 128;
-                        const int p0 = ((2 * (sub & 3)) ^ (r & 7)) << 4, p1 = ((2 * (sub & 3) + 1) ^ (r & 7)) << 4;
-                        *reinterpret_cast<uint4*>(row + p0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                        *reinterpret_cast<uint4*>(row + p1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                        if (HILO) {
-                            *reinterpret_cast<uint4*>(row + TILE + p0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                            *reinterpret_cast<uint4*>(row + TILE + p1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+#pragma unroll
+                        for (int d = 1; d < LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
+                        // the power of two below the row's largest; 127 (times one) where there is none
+                        uint32_t ex = __float_as_uint(top) >> 23;
+                        if (ex == 0 || ex >= 254) ex = 127;
+                        const float down = __uint_as_float((254u - ex) << 23);
+                        if (live) {
+                            const int r = r_at + lr;
+                            if (sub == 0) q_exp[((used & 1u) * 2 + i) * 128 + r] = (uint8_t)ex;
+                            uint32_t hi[8], lo[8];
+#pragma unroll
+                            for (int z = 0; z < 8; ++z) {
+                                const float a0 = __fmul_rn(x[2 * z], down), a1 = __fmul_rn(x[2 * z + 1], down);
+                                hi[z] = pack2<ATT_F16>(a0, a1);
+                                if (HILO) {
+                                    float h0, h1;
+                                    unpack2<ATT_F16>(hi[z], h0, h1);
+                                    lo[z] = pack2<ATT_F16>(__fsub_rn(a0, h0), __fsub_rn(a1, h1));
+                                }
+                            }
+                            uint8_t* row = q_s + (HILO ? 0 : i) * TILE + (sub / 4) * PANEL + r * 128;
+                            const int p0 = ((2 * (sub & 3)) ^ (r & 7)) << 4, p1 = ((2 * (sub & 3) + 1) ^ (r & 7)) << 4;
+                            *reinterpret_cast<uint4*>(row + p0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                            *reinterpret_cast<uint4*>(row + p1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                            if (HILO) {
+                                *reinterpret_cast<uint4*>(row + TILE + p0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                                *reinterpret_cast<uint4*>(row + TILE + p1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                            }
                         }
                     }
                 }
