@@ -15,7 +15,7 @@
 //   warps 0-3, 4-7  softmax of tile 0 and 1: a thread owns a row; S from
 //                   TMEM, P back into the same columns as 16-bit values (the A
 //                   operand of P V is read from TMEM), and the epilogue;
-//   warp 8          one lane issues tcgen05.mma: P V of block j, then Q K^T of
+//   warp 8          issues tcgen05.mma: P V of block j, then Q K^T of
 //                   block j + 1, tile 0 and tile 1 in turn;
 //   warp 9          work items and TMA: Q tiles, and a ring of K and V tiles of
 //                   128 keys (128-byte swizzle).
@@ -85,6 +85,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile PromptItem* items = reinterpret_cast<volatile PromptItem*>(tmem_slot + 2);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // a bounded wait of a whole warp
+    auto all_wait = [](uint64_t* bar, uint32_t parity, uint64_t ns) {
+        return __all_sync(FULL_MASK, mbar_wait_ns(bar, parity, ns)) != 0;
+    };
     const int TOK = 128 / a.G;                               // tokens of a query tile
 
     if (threadIdx.x == 0) {
@@ -228,72 +232,73 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     } else if (warp == 8) {
         // ---------------- tensor-core products ----------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (lane == 0) {
+        const uint32_t lead = lane == 0;
+        {
             constexpr bool BF = T == ATT_BF16;
             constexpr uint32_t ID_S = umma_idesc(BF, false, 128, PA_KEYS), ID_O = umma_idesc(BF, true, 128, D);
             uint32_t pos = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0};
-            auto wait_kv = [&](uint32_t k) { return mbar_wait_ns(&kv_full[k % NS], (k / NS) & 1u, PA_WAIT_NS); };
+            auto wait_kv = [&](uint32_t k) { return all_wait(&kv_full[k % NS], (k / NS) & 1u, PA_WAIT_NS); };
             auto scores = [&](int i, uint32_t k) {
-                const uint64_t qd = umma_desc_k(smem_u32(q_s + i * TILE)), kd = umma_desc_k(smem_u32(kv_s + (k % NS) * TILE));
+                const uint32_t qd = umma_desc_k(smem_u32(q_s + i * TILE)), kd = umma_desc_k(smem_u32(kv_s + (k % NS) * TILE));
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
                     const uint32_t off = ((d / 4) * PANEL + (d % 4) * 32) >> 4;
-                    umma_ss(tmem + 128 * i, qd + off, kd + off, ID_S, d != 0);
+                    umma_ss(tmem + 128 * i, qd + off, kd + off, ID_S, d != 0, lead);
                 }
-                umma_done(&s_full[i]);
+                umma_done(&s_full[i], lead);
             };
             auto values = [&](int i, uint32_t k, bool first) {
-                const uint64_t vd = umma_desc_mn(smem_u32(kv_s + (k % NS) * TILE), PANEL);
+                const uint32_t vd = umma_desc_mn(smem_u32(kv_s + (k % NS) * TILE), PANEL);
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < PA_KEYS / 16; ++d)
-                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, vd + 128 * d, ID_O, !first || d != 0);
+                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, vd + 128 * d, ID_O, !first || d != 0, lead);
             };
             bool ok = true;
             for (uint32_t n_item = 0; ok; ++n_item) {
                 const uint32_t slot = n_item % PA_ITEMS;
-                if (!mbar_wait_ns(&item_full[slot], (n_item / PA_ITEMS) & 1u, PA_WAIT_NS)) break;
-                const int nb[2] = {items[slot].n0, items[slot].n1};
-                mbar_arrive(&item_empty[slot]);
+                if (!all_wait(&item_full[slot], (n_item / PA_ITEMS) & 1u, PA_WAIT_NS)) break;
+                const int nb[2] = {__shfl_sync(FULL_MASK, items[slot].n0, 0), __shfl_sync(FULL_MASK, items[slot].n1, 0)};
+                if (lead) mbar_arrive(&item_empty[slot]);
                 if (nb[0] < 0) break;
                 const int n = max(nb[0], nb[1]);
                 if (n == 0) continue;
                 ok = wait_kv(pos);
                 for (int i = 0; i < 2 && ok; ++i) {
                     if (nb[i] == 0) continue;
-                    ok = mbar_wait_ns(&q_full[i], q_n[i]++ & 1u, PA_WAIT_NS);
+                    ok = all_wait(&q_full[i], q_n[i]++ & 1u, PA_WAIT_NS);
                     if (!ok) break;
                     scores(i, pos);
-                    if (nb[i] == 1) umma_done(&q_empty[i]);
+                    if (nb[i] == 1) umma_done(&q_empty[i], lead);
                 }
                 if (!ok) break;
-                umma_done(&kv_empty[pos % NS]);
+                umma_done(&kv_empty[pos % NS], lead);
                 for (int j = 0; j < n && ok; ++j) {
                     const uint32_t kv = pos + 2 * j + 1;                 // V of block j; K of block j + 1 follows
                     ok = wait_kv(kv);
                     for (int i = 0; i < 2 && ok; ++i) {
                         if (j >= nb[i]) continue;
-                        ok = mbar_wait_ns(&p_ready[i], p_n[i]++ & 1u, PA_WAIT_NS);
+                        ok = all_wait(&p_ready[i], p_n[i]++ & 1u, PA_WAIT_NS);
                         if (!ok) break;
                         values(i, kv, j == 0);
-                        if (j + 1 == nb[i]) umma_done(&o_full[i]);
+                        if (j + 1 == nb[i]) umma_done(&o_full[i], lead);
                         if (j + 1 < nb[i]) {
                             ok = wait_kv(kv + 1);
                             if (!ok) break;
                             scores(i, kv + 1);
-                            if (j + 2 == nb[i]) umma_done(&q_empty[i]);
+                            if (j + 2 == nb[i]) umma_done(&q_empty[i], lead);
                         }
                     }
                     if (!ok) break;
-                    umma_done(&kv_empty[kv % NS]);
-                    if (j + 1 < n) umma_done(&kv_empty[(kv + 1) % NS]);
+                    umma_done(&kv_empty[kv % NS], lead);
+                    if (j + 1 < n) umma_done(&kv_empty[(kv + 1) % NS], lead);
                 }
                 pos += 2 * n;
             }
             // every product has completed before TMEM is released
-            umma_done(drain);
-            mbar_wait_ns(drain, 0u, PA_WAIT_NS);
+            umma_done(drain, lead);
+            all_wait(drain, 0u, PA_WAIT_NS);
         }
     } else if (warp < 8) {
         // ---------------- softmax and epilogue ----------------

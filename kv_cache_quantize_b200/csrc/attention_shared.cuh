@@ -23,7 +23,7 @@
 //   warps 8-11       keys and values: 16-byte asynchronous copies through the
 //                    page lists, any page size; int8 codes are turned into f16
 //                    (exactly) on their way into the product's tiles;
-//   warp 12          one lane issues tcgen05.mma;
+//   warp 12          issues tcgen05.mma;
 //   warp 13          cuts the work, and loads Q where it needs no scaling;
 //   warps 14, 15     scale Q over int8 caches, tile 0 and 1, for the next piece
 //                    while the tiles' last steps run.
@@ -165,6 +165,10 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     volatile SharedItem* items = reinterpret_cast<volatile SharedItem*>(tmem_slot + 2 + SA_BAD + 4 * SA_BAD);
     int* s_blocks = reinterpret_cast<int*>(tmem_slot + 1);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    // a bounded wait of a whole warp
+    auto all_wait = [](uint64_t* bar, uint32_t parity, uint64_t ns) {
+        return __all_sync(FULL_MASK, mbar_wait_ns(bar, parity, ns)) != 0;
+    };
     const int TOK = 128 / a.G;
 
     if (smem_u32(smem) & 1023u) {                            // uniform over the grid; never on this hardware
@@ -334,76 +338,77 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     } else if (warp == 12) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---------------- tensor-core products ----------------
-        if (lane == 0) {
+        const uint32_t lead = lane == 0;
+        {
             constexpr bool BF = MT == ATT_BF16;
             constexpr uint32_t ID_S = umma_idesc(BF, false, 128, SA_KEYS), ID_O = umma_idesc(BF, true, 128, D);
             uint32_t pos = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0};
-            auto wait_kv = [&](uint32_t k) { return mbar_wait_ns(&kv_full[k % NS], (k / NS) & 1u, SA_WAIT_NS); };
+            auto wait_kv = [&](uint32_t k) { return all_wait(&kv_full[k % NS], (k / NS) & 1u, SA_WAIT_NS); };
             auto scores = [&](int i, uint32_t k) {
-                const uint64_t qd = umma_desc_k(smem_u32(q_s + (HILO ? 0 : i) * TILE));
-                const uint64_t kd = umma_desc_k(smem_u32(kv_s + (k % NS) * TILE));
+                const uint32_t qd = umma_desc_k(smem_u32(q_s + (HILO ? 0 : i) * TILE));
+                const uint32_t kd = umma_desc_k(smem_u32(kv_s + (k % NS) * TILE));
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
                     const uint32_t off = ((d / 4) * PANEL + (d % 4) * 32) >> 4;
-                    umma_ss(tmem + 128 * i, qd + off, kd + off, ID_S, d != 0);
-                    if (HILO) umma_ss(tmem + 128 * i, qd + (TILE >> 4) + off, kd + off, ID_S, true);
+                    umma_ss(tmem + 128 * i, qd + off, kd + off, ID_S, d != 0, lead);
+                    if (HILO) umma_ss(tmem + 128 * i, qd + (TILE >> 4) + off, kd + off, ID_S, true, lead);
                 }
-                umma_done(&s_full[i]);
+                umma_done(&s_full[i], lead);
             };
             auto values = [&](int i, uint32_t k, bool first) {
-                const uint64_t vd = umma_desc_mn(smem_u32(kv_s + (k % NS) * TILE), PANEL);
+                const uint32_t vd = umma_desc_mn(smem_u32(kv_s + (k % NS) * TILE), PANEL);
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < SA_KEYS / 16; ++d)
-                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, vd + 128 * d, ID_O, !first || d != 0);
+                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, vd + 128 * d, ID_O, !first || d != 0, lead);
             };
             bool ok = true;
             for (uint32_t n_item = 0; ok; ++n_item) {
                 const uint32_t slot = n_item % SA_ITEMS;
-                if (!mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS)) break;
-                const int n = items[slot].steps;
-                const bool alt = items[slot].alt != 0;
-                mbar_arrive(&item_empty[slot]);
+                if (!all_wait(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS)) break;
+                const int n = __shfl_sync(FULL_MASK, items[slot].steps, 0);
+                const bool alt = __shfl_sync(FULL_MASK, items[slot].alt, 0) != 0;
+                if (lead) mbar_arrive(&item_empty[slot]);
                 if (n < 0) break;
                 // the first scores of each tile
                 for (int i = 0; i < 2 && ok; ++i) {
                     const int s = alt ? i : 0;
                     if (s >= n) break;
-                    if (!HILO || i == 0) ok = mbar_wait_ns(&q_full[i], q_n[i]++ & 1u, SA_WAIT_NS);
+                    if (!HILO || i == 0) ok = all_wait(&q_full[i], q_n[i]++ & 1u, SA_WAIT_NS);
                     ok = ok && wait_kv(pos + k_pos(s));
                     if (!ok) break;
                     scores(i, pos + k_pos(s));
-                    if (alt) umma_done(&kv_empty[(pos + k_pos(s)) % NS]);
-                    if (!HILO && (alt ? s + 2 >= n : n == 1)) umma_done(&q_empty[i]);
+                    if (alt) umma_done(&kv_empty[(pos + k_pos(s)) % NS], lead);
+                    if (!HILO && (alt ? s + 2 >= n : n == 1)) umma_done(&q_empty[i], lead);
                 }
-                if (ok && !alt) umma_done(&kv_empty[pos % NS]);
+                if (ok && !alt) umma_done(&kv_empty[pos % NS], lead);
                 for (int s = 0; s < n && ok; ++s) {
                     const uint32_t v = pos + v_pos(s, n);
                     ok = wait_kv(v);
                     for (int i = alt ? s & 1 : 0; i < (alt ? (s & 1) + 1 : 2) && ok; ++i) {
-                        ok = mbar_wait_ns(&p_ready[i], p_n[i]++ & 1u, SA_WAIT_NS);
+                        ok = all_wait(&p_ready[i], p_n[i]++ & 1u, SA_WAIT_NS);
                         if (!ok) break;
                         values(i, v, s < (alt ? 2 : 1));
                         const int nx = s + (alt ? 2 : 1);
                         if (nx >= n) {
-                            umma_done(&o_full[i]);
+                            umma_done(&o_full[i], lead);
                         } else {
                             const uint32_t k = pos + k_pos(nx);
                             ok = wait_kv(k);
                             if (!ok) break;
                             scores(i, k);
-                            if (alt || i == 1) umma_done(&kv_empty[k % NS]);
-                            if (!HILO && nx + (alt ? 2 : 1) >= n) umma_done(&q_empty[i]);
+                            if (alt || i == 1) umma_done(&kv_empty[k % NS], lead);
+                            if (!HILO && nx + (alt ? 2 : 1) >= n) umma_done(&q_empty[i], lead);
                         }
                     }
-                    if (ok) umma_done(&kv_empty[v % NS]);
+                    if (ok) umma_done(&kv_empty[v % NS], lead);
                 }
-                if (HILO && ok) umma_done(&q_empty[0]);
+                if (HILO && ok) umma_done(&q_empty[0], lead);
                 pos += 2 * n;
             }
-            umma_done(drain);
-            mbar_wait_ns(drain, 0u, SA_WAIT_NS);
+            umma_done(drain, lead);
+            all_wait(drain, 0u, SA_WAIT_NS);
         }
     } else if (warp >= 14) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");

@@ -136,44 +136,55 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, i
         : "memory");
 }
 
+// Matrix descriptors of 16-bit tiles in 128-byte rows (64 values) with the
+// 128-byte swizzle, 8-row groups 1024 bytes apart (stride byte offset): their
+// upper half is the same for all, the lower one holds the address and the
+// leading byte offset.
+// K-major (Q, K): a row is one M / N index, its 64 values run along K; the
+// leading offset is not used.  The k-th 16 values start 32 k bytes in.
+constexpr uint32_t UMMA_DESC_HI = (1024u >> 4) | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t umma_desc_k(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | 1u << 16; }
+// MN-major (V): a row is one K index, its 64 values run along N; the next 64
+// N values are a panel of `panel` bytes further (leading byte offset).  The
+// k-th 16 rows start 2048 k bytes in.
+__device__ __forceinline__ uint32_t umma_desc_mn(uint32_t saddr, uint32_t panel) {
+    return ((saddr & 0x3FFFFu) >> 4) | (panel >> 4) << 16;
+}
+
+// The products are issued by one lane (`lead` nonzero) of a converged warp,
+// not inside a branch of that lane: the descriptors then live in uniform
+// registers.  In a branch they are moved there product by product, and the
+// warp takes longer to issue the products than the tensor core to run them.
+
 // D[tmem] (+)= A[smem] B[smem]
-__device__ __forceinline__ void umma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void umma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 a, {%1, %6};\n\tmov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(lead), "n"(UMMA_DESC_HI)
         : "memory");
 }
 
 // D[tmem] (+)= A[tmem] B[smem]: A's row i in lane i, two 16-bit k values per column
-__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool acc) {
+__device__ __forceinline__ void umma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool acc, uint32_t lead) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)acc)
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 q, %5, 0;\n\t"
+        "mov.b64 b, {%2, %6};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], b, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)acc), "r"(lead), "n"(UMMA_DESC_HI)
         : "memory");
 }
 
-// one arrival on bar once every tcgen05.mma this thread issued before has completed
-__device__ __forceinline__ void umma_done(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
-// Matrix descriptors of 16-bit tiles in 128-byte rows (64 values) with the
-// 128-byte swizzle, 8-row groups 1024 bytes apart (stride byte offset).
-// K-major (Q, K): a row is one M / N index, its 64 values run along K; the
-// leading offset is not used.  The k-th 16 values start 32 k bytes in.
-__device__ __forceinline__ uint64_t umma_desc_k(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)1 << 16 | (uint64_t)(1024u >> 4) << 32 | (uint64_t)1 << 46 |
-           (uint64_t)2 << 61;
-}
-// MN-major (V): a row is one K index, its 64 values run along N; the next 64
-// N values are a panel of `panel` bytes further (leading byte offset).  The
-// k-th 16 rows start 2048 k bytes in.
-__device__ __forceinline__ uint64_t umma_desc_mn(uint32_t saddr, uint32_t panel) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(panel >> 4) << 16 | (uint64_t)(1024u >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+// one arrival on bar once every tcgen05.mma the leading lane issued before has completed
+__device__ __forceinline__ void umma_done(uint64_t* bar, uint32_t lead) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(lead)
+        : "memory");
 }
 
 // Instruction descriptor, kind::f16, fp32 accumulator: A and B bf16 or f16, A
