@@ -116,7 +116,15 @@ __device__ __forceinline__ void att_store(uint8_t* p, int64_t i, float v) {
     else reinterpret_cast<__half*>(p)[i] = __float2half_rn(v);
 }
 
-// the exponent bits of two packed 16-bit values: nonzero where one is not finite
+// nonzero if one of eight packed 16-bit values is not finite: adding one to an
+// exponent of ones carries into the sign bit, and no further
+template <int T>
+__device__ __forceinline__ uint32_t any_not_finite(uint4 v) {
+    constexpr uint32_t E = T == ATT_BF16 ? 0x7F807F80u : 0x7C007C00u, ONE = T == ATT_BF16 ? 0x00800080u : 0x04000400u;
+    return (((v.x & E) + ONE) | ((v.y & E) + ONE) | ((v.z & E) + ONE) | ((v.w & E) + ONE)) & 0x80008000u;
+}
+
+// all bits of those of two packed 16-bit values that are not finite
 template <int T>
 __device__ __forceinline__ uint32_t not_finite2(uint32_t w) {
     constexpr uint32_t E = T == ATT_BF16 ? 0x7F807F80u : 0x7C007C00u;

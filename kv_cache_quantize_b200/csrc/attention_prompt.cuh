@@ -336,28 +336,31 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 ok = __all_sync(FULL_MASK, mbar_wait_ns(&s_full[i], s_n++ & 1u, PA_WAIT_NS));
                 if (!ok) break;
                 tm_fence_after();
+                const int key0 = j * PA_KEYS;
+                if (key0 + PA_KEYS > low || flip) {
+                    // the less common cases are put right in TMEM, to keep the common code short:
+                    // keys that the row does not see, a negative scale
+                    const int see = lim - key0;
+#pragma unroll 1
+                    for (int k0 = 0; k0 < PA_KEYS; k0 += 32) {
+                        const uint32_t have = see - k0 >= 32 ? 0xFFFFFFFFu : see > k0 ? (1u << (see - k0)) - 1u : 0u;
+                        uint32_t x[32];
+                        tm_ld32(s_t + k0, x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) x[k] = (have >> k) & 1u ? x[k] ^ flip : 0xFF800000u;
+                        tm_st32(s_t + k0, x);
+                    }
+                    tm_wait_st();
+                }
                 uint32_t s[128];
                 tm_ld128(s_t, s);
-                if (flip) {
+                float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-                    for (int k = 0; k < 128; ++k) s[k] ^= flip;
-                }
-                const int key0 = j * PA_KEYS;
-                if (key0 + PA_KEYS > low) {
-                    const int see = lim - key0;
-#pragma unroll
-                    for (int k = 0; k < 128; ++k)
-                        if (k >= see) s[k] = 0xFF800000u;    // -inf
-                }
-                float mx[4] = {__uint_as_float(s[0]), __uint_as_float(s[1]), __uint_as_float(s[2]), __uint_as_float(s[3])};
-#pragma unroll
-                for (int k = 4; k < 124; k += 8) {
+                for (int k = 0; k < 128; k += 8) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
                         mx[q] = max3(mx[q], __uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1]));
                 }
-#pragma unroll
-                for (int q = 0; q < 4; ++q) mx[q] = fmaxf(mx[q], __uint_as_float(s[124 + q]));
                 const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
                 // the row's own reference moves only when its maximum has outgrown it
                 const bool grow = __fmul_rn(__fsub_rn(bm, m), c) > PA_SLACK || (m == -INFINITY && bm > m);
@@ -407,25 +410,28 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     if (!ok) break;
                     uint8_t* vs = kv_s + (vp % NS) * TILE;
                     const int r0 = max(low - key0, 0), end = w.lk - key0;
-                    bool bad = false;
+                    uint32_t bad = 0;
+#pragma unroll 2
                     for (int k = r0 * 8 + r; k < PA_KEYS * 8; k += 128) {
 #pragma unroll
                         for (int p = 0; p < PANELS; ++p) {
                             uint4* e = reinterpret_cast<uint4*>(vs + p * PANEL + k * 16);
-                            if ((k >> 3) >= end) {
-                                *e = make_uint4(0u, 0u, 0u, 0u);
-                            } else {
-                                uint4 v = *e;
-                                const uint32_t b0 = not_finite2<T>(v.x), b1 = not_finite2<T>(v.y),
-                                               b2 = not_finite2<T>(v.z), b3 = not_finite2<T>(v.w);
-                                if (b0 | b1 | b2 | b3) {
-                                    bad = true;
-                                    *e = make_uint4(v.x & ~b0, v.y & ~b1, v.z & ~b2, v.w & ~b3);
-                                }
+                            if ((k >> 3) >= end) *e = make_uint4(0u, 0u, 0u, 0u);
+                            else bad |= any_not_finite<T>(*e);
+                        }
+                    }
+                    if (bad) {
+                        // take them out (this thread's pieces of V)
+                        items[slot].dirty = 1;
+#pragma unroll 1
+                        for (int k = r0 * 8 + r; k < PA_KEYS * 8; k += 128) {
+#pragma unroll 1
+                            for (int q = 0; q < 4 * PANELS; ++q) {
+                                uint32_t* e = reinterpret_cast<uint32_t*>(vs + (q >> 2) * PANEL + k * 16) + (q & 3);
+                                *e &= ~not_finite2<T>(*e);
                             }
                         }
                     }
-                    if (bad) items[slot].dirty = 1;
                     fence_proxy_async_smem();
                 }
                 tm_wait_st();
@@ -451,19 +457,6 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 float v[32];
 #pragma unroll
                 for (int q = 0; q < 32; ++q) v[q] = lim > 0 ? __fmul_rn(__uint_as_float(o[q]), inv) : 0.0f;
-                if (dirty && live) {
-                    // low of the tile that took them out: tile 0's, or tile 1's where tile 0 has no such block
-                    for (int key = a.causal ? max(w.lim0, 0) : w.lk; key < lim; ++key) {
-                        const uint8_t* vr = a.v.base + ((w.k0 + (int64_t)key) * a.v.tok + w.kh * a.v.head + k) * 2;
-#pragma unroll
-                        for (int q = 0; q < 16; ++q) {
-                            const uint32_t e = reinterpret_cast<const uint32_t*>(vr)[q];
-                            const uint32_t b = not_finite2<T>(e);
-                            if (b & 0xFFFFu) v[2 * q] = __fadd_rn(v[2 * q], att_load<T>(vr, 2 * q));
-                            if (b >> 16) v[2 * q + 1] = __fadd_rn(v[2 * q + 1], att_load<T>(vr, 2 * q + 1));
-                        }
-                    }
-                }
                 if (live) {
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
@@ -473,6 +466,18 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                         e.z = pack2<T>(v[8 * q + 4], v[8 * q + 5]);
                         e.w = pack2<T>(v[8 * q + 6], v[8 * q + 7]);
                         reinterpret_cast<uint4*>(out + 2 * k)[q] = e;
+                    }
+                }
+            }
+            if (dirty && live) {
+                // give back to this row what was taken out of V and the row sees
+                for (int key = a.causal ? max(w.lim0, 0) : w.lk; key < lim; ++key) {
+                    const uint8_t* vr = a.v.base + ((w.k0 + (int64_t)key) * a.v.tok + w.kh * a.v.head) * 2;
+#pragma unroll 1
+                    for (int d = 0; d < D; d += 2) {
+                        const uint32_t b = not_finite2<T>(*reinterpret_cast<const uint32_t*>(vr + 2 * d));
+                        if (b & 0xFFFFu) att_store<T>(out, d, __fadd_rn(att_load<T>(out, d), att_load<T>(vr, d)));
+                        if (b >> 16) att_store<T>(out, d + 1, __fadd_rn(att_load<T>(out, d + 1), att_load<T>(vr, d + 1)));
                     }
                 }
             }
