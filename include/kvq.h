@@ -318,8 +318,10 @@ KVQ_API kvq_status kvq_compressor(const kvq_tensor* x, const kvq_tensor* w_kv, c
 /* cu_seqlens_q, cu_seqlens_k   int32 [B + 1], contiguous: sequence b holds   */
 /*          the rows [cu[b], cu[b + 1]).  cu_seqlens_k NULL: as the queries.  */
 /*          Both NULL for the 4-D form.  Rows of out that no sequence holds   */
-/*          keep their contents; a span outside the tensor counts as an empty */
-/*          sequence and sets KVQ_FAULT_SLOT_RANGE.                            */
+/*          keep their contents.  A span that is negative or not inside the   */
+/*          tensor counts as an empty sequence and sets KVQ_FAULT_SLOT_RANGE  */
+/*          (rows of other sequences may then be left unwritten where the     */
+/*          offsets make them overlap).                                        */
 /* causal   nonzero: query i of a sequence with lq queries and lk keys sees   */
 /*          the keys j <= i + lk - lq (its own token is the last one it sees, */
 /*          also behind a cached context); 0: every key of the sequence.      */

@@ -82,8 +82,8 @@ kvq_status run_prompt(const PromptArgs& a, cudaStream_t s) {
     const int64_t items = (a.T / (2 * tok) + a.B) * a.Nkv;       // at least the number of work items
     auto kernel = prompt_kernel<T, D>;
     constexpr uint32_t smem = pa_smem_bytes(D);
-    return launched(launch(kernel, (unsigned)persistent_grid(kernel, PA_THREADS, items, smem), PA_THREADS, smem, s, mq, mk,
-                           mv, a));
+    resident_blocks(reinterpret_cast<const void*>(kernel), PA_THREADS, smem);    // raises the shared-memory limit once
+    return launched(launch(kernel, (unsigned)items, PA_THREADS, smem, s, mq, mk, mv, a));
 }
 
 // How the work is laid out, and the workspace in bytes.  The size is that of
@@ -205,6 +205,7 @@ kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k, const 
     a.G = (int32_t)(Nq / Nkv);
     a.D = (int32_t)D;
     a.causal = causal != 0;
+    a.out32 = reinterpret_cast<uintptr_t>(out->data) % 32 == 0 && a.out.tok % 16 == 0 && a.out.head % 16 == 0;
     a.scale = softmax_scale;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     if (type == ATT_BF16) return D == 64 ? run_prompt<ATT_BF16, 64>(a, s) : run_prompt<ATT_BF16, 128>(a, s);

@@ -35,6 +35,7 @@ struct PromptArgs {
     int32_t B;
     int32_t Nq, Nkv, G, D;
     int32_t causal;
+    int32_t out32;                 // rows of out are 32-byte aligned
     float scale;                   // softmax scale
 };
 
@@ -152,9 +153,19 @@ __device__ __forceinline__ void unpack2(uint32_t w, float& lo, float& hi) {
     }
 }
 
+// 32 bytes in one store (32-byte aligned): a lane that writes a row of its own
+// takes the store unit a cycle for each store, whatever its width
+__device__ __forceinline__ void store32(void* p, uint32_t a, uint32_t b, uint32_t c, uint32_t d, uint32_t e, uint32_t f,
+                                        uint32_t g, uint32_t h) {
+    asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(a), "r"(b), "r"(c), "r"(d),
+                 "r"(e), "r"(f), "r"(g), "r"(h)
+                 : "memory");
+}
+
+// the largest of three; NaN if one is
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float d;
-    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
     return d;
 }
 

@@ -17,7 +17,9 @@
 //                   operand of P V is read from TMEM), and the epilogue;
 //   warp 8          issues tcgen05.mma: P V of block j, then Q K^T of
 //                   block j + 1, tile 0 and tile 1 in turn;
-//   warp 9          work items and TMA: Q tiles, and a ring of K and V tiles of
+//   warp 9          work items and TMA: the grid has a CTA for every item, but a
+//                   running CTA takes over items whose CTAs have not started
+//                   (cluster launch control), heavy ones first; Q tiles, and a ring of K and V tiles of
 //                   128 keys (128-byte swizzle).
 // The tensor pipe executes a CTA's products in order, so Q K^T of block j + 1
 // may overwrite the columns that P V of block j reads.
@@ -81,9 +83,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
     uint64_t* item_empty = item_full + PA_ITEMS;
     uint64_t* kv_full = item_empty + PA_ITEMS;
     uint64_t* kv_empty = kv_full + NS;
-    uint64_t* drain = kv_empty + NS;
+    uint64_t* next_item = kv_empty + NS;
+    uint64_t* drain = next_item + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile PromptItem* items = reinterpret_cast<volatile PromptItem*>(tmem_slot + 2);
+    uint8_t* taken = smem + (2 + NS) * TILE + 496;           // 16 bytes: which CTA's work was taken over
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     // a bounded wait of a whole warp
     auto all_wait = [](uint64_t* bar, uint32_t parity, uint64_t ns) {
@@ -107,6 +111,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             mbar_init(&kv_full[i], 1);
             mbar_init(&kv_empty[i], 1);
         }
+        mbar_init(next_item, 1);
         mbar_init(drain, 1);
         mbar_init_fence();
     }
@@ -123,23 +128,27 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         // ---------------- work items and loads ----------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const uint32_t q_bytes = (uint32_t)(TOK * a.G) * 128u * PANELS;
-        uint32_t pos = 0, n_item = 0, q_n[2] = {0, 0};
+        uint32_t pos = 0, n_item = 0, n_asked = 0, q_n[2] = {0, 0};
         int cb = 0;
         int64_t cbase = 0;                                   // tiles of the sequences before cb
         bool dead = false;
-        for (uint32_t pass = 0; !dead; ++pass) {
-            const int64_t it = (int64_t)pass * gridDim.x + ((pass & 1u) ? gridDim.x - 1 - blockIdx.x : blockIdx.x);
+        int64_t it = blockIdx.x;
+        while (!dead) {
             const int64_t x = it / a.Nkv;
+            if (x < cbase) {                                 // items come in ascending order; if not, start over
+                cb = 0;
+                cbase = 0;
+            }
             // the sequence and tile of item x: the cursor only moves forward
             bool found = false;
             SeqSpan sp = {0, 0, 0, 0};
             int32_t local = 0, ntiles = 0;
-            while (!found && cb < a.B) {
+            while (it >= 0 && !found && cb < a.B) {
                 const int b = cb + lane;
                 int32_t nt = 0;
                 SeqSpan s = {0, 0, 0, 0};
                 if (b < a.B) {
-                    s = prompt_span(a, b, blockIdx.x == 0);
+                    s = prompt_span(a, b, true);
                     nt = (s.lq + 2 * TOK - 1) / (2 * TOK);
                 }
                 int32_t incl = nt;
@@ -163,10 +172,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     cb += 32;
                 }
             }
+            if (it >= 0 && lane == 0) take_over(taken, next_item);
             PromptItem w;
             w.n0 = -1;
             w.n1 = 0;
-            w.dirty = 0;
             if (found) {
                 const int32_t t0 = (ntiles - 1 - local) * 2 * TOK;       // the longest rows first
                 w.tok0 = (int32_t)sp.q0 + t0;
@@ -180,24 +189,27 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 w.n0 = m0 > 0 ? (m0 + PA_KEYS - 1) / PA_KEYS : 0;
                 w.n1 = nt1 > 0 && m1 > 0 ? (m1 + PA_KEYS - 1) / PA_KEYS : 0;
             }
-            const uint32_t slot = n_item % PA_ITEMS;
-            if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_empty[slot], ((n_item / PA_ITEMS) & 1u) ^ 1u, PA_WAIT_NS))) break;
-            if (lane == 0) {
-                volatile PromptItem& o = items[slot];
-                o.n0 = w.n0;
-                o.n1 = w.n1;
-                o.tok0 = w.tok0;
-                o.ntok = w.ntok;
-                o.lim0 = w.lim0;
-                o.lk = w.lk;
-                o.k0 = w.k0;
-                o.kh = w.kh;
-                o.dirty = 0;
-                mbar_arrive(&item_full[slot]);
+            // (the grid may have a few CTAs more than there are items)
+            if (found || it < 0) {
+                const uint32_t slot = n_item % PA_ITEMS;
+                if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_empty[slot], ((n_item / PA_ITEMS) & 1u) ^ 1u, PA_WAIT_NS))) break;
+                if (lane == 0) {
+                    volatile PromptItem& o = items[slot];
+                    o.n0 = w.n0;
+                    o.n1 = w.n1;
+                    o.tok0 = w.tok0;
+                    o.ntok = w.ntok;
+                    o.lim0 = w.lim0;
+                    o.lk = w.lk;
+                    o.k0 = w.k0;
+                    o.kh = w.kh;
+                    o.dirty = 0;
+                    mbar_arrive(&item_full[slot]);
+                }
+                ++n_item;
+                if (it < 0) break;
             }
-            ++n_item;
-            if (w.n0 < 0) break;
-            if (lane == 0) {
+            if (found && lane == 0) {
                 const int n = max(w.n0, w.n1);
                 auto load_q = [&](int i) {
                     if ((i ? w.n1 : w.n0) == 0) return true;
@@ -221,6 +233,11 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 for (int j = 1; j < n && !dead; ++j) dead = !load_kv(&tm_k, j) || !load_kv(&tm_v, j);
             }
             dead = __shfl_sync(FULL_MASK, dead, 0);
+            // the answer to the request is there by now
+            if (!__all_sync(FULL_MASK, mbar_wait_ns(next_item, n_asked++ & 1u, PA_WAIT_NS))) break;
+            it = taken_over(taken);
+            __syncwarp();
+            fence_proxy_async_smem();                        // read before the next answer is written
         }
         // no load may still be in flight when the CTA exits
         if (lane == 0) {
@@ -361,9 +378,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     for (int q = 0; q < 4; ++q)
                         mx[q] = max3(mx[q], __uint_as_float(s[k + 2 * q]), __uint_as_float(s[k + 2 * q + 1]));
                 }
-                const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
+                const float bm = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
                 // the row's own reference moves only when its maximum has outgrown it
-                const bool grow = __fmul_rn(__fsub_rn(bm, m), c) > PA_SLACK || (m == -INFINITY && bm > m);
+                // (or is NaN, which then stays)
+                const bool grow = !(__fmul_rn(__fsub_rn(bm, m), c) <= PA_SLACK) && bm != -INFINITY;
                 if (j == 0) {
                     m = bm;
                 } else if (__any_sync(FULL_MASK, grow)) {
@@ -457,15 +475,17 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 float v[32];
 #pragma unroll
                 for (int q = 0; q < 32; ++q) v[q] = lim > 0 ? __fmul_rn(__uint_as_float(o[q]), inv) : 0.0f;
-                if (live) {
+                uint32_t x[16];
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        uint4 e;
-                        e.x = pack2<T>(v[8 * q], v[8 * q + 1]);
-                        e.y = pack2<T>(v[8 * q + 2], v[8 * q + 3]);
-                        e.z = pack2<T>(v[8 * q + 4], v[8 * q + 5]);
-                        e.w = pack2<T>(v[8 * q + 6], v[8 * q + 7]);
-                        reinterpret_cast<uint4*>(out + 2 * k)[q] = e;
+                for (int z = 0; z < 16; ++z) x[z] = pack2<T>(v[2 * z], v[2 * z + 1]);
+                if (live) {
+                    if (a.out32) {
+                        store32(out + 2 * k, x[0], x[1], x[2], x[3], x[4], x[5], x[6], x[7]);
+                        store32(out + 2 * k + 32, x[8], x[9], x[10], x[11], x[12], x[13], x[14], x[15]);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            reinterpret_cast<uint4*>(out + 2 * k)[q] = make_uint4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
                     }
                 }
             }

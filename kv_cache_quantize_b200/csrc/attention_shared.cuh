@@ -696,8 +696,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                                 mx[q] = max3(mx[q], __uint_as_float(x[k + 2 * q]), __uint_as_float(x[k + 2 * q + 1]));
                         }
                     }
-                    const float bm = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]);
-                    const bool grow = __fmul_rn(__fsub_rn(bm, m), c) > SA_SLACK || (m == -INFINITY && bm > m);
+                    const float bm = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
+                    const bool grow = !(__fmul_rn(__fsub_rn(bm, m), c) <= SA_SLACK) && bm != -INFINITY;
                     if (s == first) {
                         m = bm;
                     } else if (__any_sync(FULL_MASK, grow)) {
@@ -771,8 +771,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 }
                 if (live) {
                     float2* st = reinterpret_cast<float2*>(ws + (w.own ? plan.own_stats : plan.stats_area)) + row;
-                    // a row of NaN scores has no maximum: its sum, NaN, must still count
-                    *st = make_float2(m == -INFINITY ? (l != l ? 0.0f : m) : __fmaf_rn(m, c, -SHIFT), l);
+                    // a row with a NaN score has no maximum, but its sum, NaN, must count
+                    *st = make_float2(l != l ? 0.0f : m == -INFINITY ? m : __fmaf_rn(m, c, -SHIFT), l);
                 }
             }
             tm_fence_before();

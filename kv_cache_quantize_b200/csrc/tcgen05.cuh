@@ -195,4 +195,29 @@ __host__ __device__ constexpr uint32_t umma_idesc(bool bf16, bool b_mn, int M, i
            ((uint32_t)(M >> 4) << 24);
 }
 
+// Cluster launch control: ask for the work of a CTA of this grid that has not
+// started (16 bytes to `slot`, counted on `bar`), and read the answer: that
+// CTA's number, or -1 when there is none left.
+__device__ __forceinline__ void take_over(void* slot, uint64_t* bar) {
+    mbar_arrive_expect_tx(bar, 16);
+    asm volatile(
+        "clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(
+            smem_u32(slot)),
+        "r"(smem_u32(bar))
+        : "memory");
+}
+__device__ __forceinline__ int64_t taken_over(const void* slot) {
+    uint32_t ok, x;
+    asm volatile(
+        "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\t"
+        "ld.shared.b128 h, [%2];\n\t"
+        "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+        "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+        : "=r"(ok), "=r"(x)
+        : "r"(smem_u32(slot))
+        : "memory");
+    return ok ? (int64_t)x : -1;
+}
+
 }  // namespace kvq
