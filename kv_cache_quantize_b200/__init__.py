@@ -1,9 +1,9 @@
 """B200-native per-token KV-cache epilogue, and the attention and page operations
 on its caches: Python binding of libkvq.so.
 
-Thin ctypes marshalling over the C ABI in include/kvq.h -- every step of the
-epilogue runs in the library's sm_100a kernels; torch supplies device memory
-and streams only.  There is no fallback: if the CUDA library is missing, the
+Thin marshalling over the C ABI in include/kvq.h (ctypes; an extension module
+for the calls that run with every layer) -- every step runs in the library's
+sm_100a kernels; torch supplies device memory and streams only.  There is no fallback: if the CUDA library is missing, the
 first call raises.
 
 Operations (same names as the C ABI without the ``kvq_`` prefix):
@@ -24,8 +24,8 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import importlib.util
 import os
-import struct
 from typing import Optional, Sequence, Tuple
 
 import torch
@@ -42,6 +42,7 @@ __all__ = [
 _HERE = os.path.dirname(os.path.abspath(__file__))
 library_path = os.path.join(_HERE, "libkvq.so")
 _LIB: Optional[ctypes.CDLL] = None
+_CALLS = None
 
 MAX_DIMS = 8
 FAULT_SLOT_RANGE = 0x1
@@ -342,77 +343,37 @@ def scatter_rows(x: torch.Tensor, slot_mapping: torch.Tensor, cache: torch.Tenso
 
 
 # ---------------------------------------------------------------------------
-# Attention and page operations.  These run once per layer and step, where a
-# few microseconds on the host count: their descriptors are packed into one
-# buffer with struct instead of one ctypes object each.
-_DESC = [struct.Struct("@Pii" + f"{n}q{8 * (MAX_DIMS - n)}x" + f"{n}q{8 * (MAX_DIMS - n)}x")
-         for n in range(MAX_DIMS + 1)]
-_DESC_BYTES = ctypes.sizeof(KvqTensor)
+# Attention and page operations, through the extension module _calls (see csrc/calls.cpp).
+def _calls():
+    global _CALLS
+    if _CALLS is None:
+        lib()                                  # the library it is linked to
+        path = os.path.join(_HERE, "_calls.so")
+        if not os.path.exists(path):
+            raise RuntimeError(f"extension not built: {path} is missing "
+                               "(run `python -c 'import __graft_entry__ as g; g.build()'`)")
+        spec = importlib.util.spec_from_file_location("_calls", path)
+        _CALLS = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_CALLS)
+    return _CALLS
 
 
-def _pack(op: str, tensors, device: Optional[torch.device]):
-    """Descriptors of the tensors (None allowed) side by side: the buffer, their
-    addresses (None for None), and their one CUDA device."""
-    buf = bytearray(_DESC_BYTES * len(tensors))
-    base = ctypes.addressof((ctypes.c_char * len(buf)).from_buffer(buf)) if tensors else 0
-    at = []
-    off = 0
-    for t in tensors:
-        if t is None:
-            at.append(None)
-            continue
-        if type(t) is not torch.Tensor and not isinstance(t, torch.Tensor):
-            raise TypeError(f"{op}: expected a tensor, got {type(t).__name__}")
-        code = _DTYPES.get(t.dtype)
-        if code is None:
-            raise TypeError(f"dtype {t.dtype} has no kvq equivalent")
-        shape = t.shape
-        n = len(shape)
-        if n > MAX_DIMS:
-            raise ValueError("too many dimensions")
-        ptr = t.data_ptr()
-        if 0 in shape:
-            ptr = 0
-        else:
-            dev = t.device
-            if dev != device:
-                if dev.type != "cuda":
-                    raise ValueError(f"{op}: tensors must be on a CUDA device, got one on {dev}")
-                if device is not None:
-                    raise ValueError(f"{op}: tensors on {device} and {dev}; all must be on one device")
-                device = dev
-        _DESC[n].pack_into(buf, off, ptr, code, n, *shape, *t.stride())
-        at.append(base + off)
-        off += _DESC_BYTES
-    return buf, at, device
+def _done(op: str, answer, check: bool):
+    """The result of a call, or its error: (status, stream, result)."""
+    status, stream, result = answer
+    if status:
+        raise KvqError(op, status)
+    if check:
+        _faults(op, True, stream)
+    return result
 
 
-def _run(op: str, call, stream, check: bool, dev: Optional[torch.device]) -> None:
-    """Call the library with the device current and the stream chosen as for every operation."""
-    with _on(dev):
-        if stream is None:
-            st = torch.cuda.current_stream(dev).cuda_stream if dev is not None else 0
-        else:
-            st = _stream(stream)
-        _check(op, call(st))
-        _faults(op, check, st)
-
-
-def _using(stream, device):
-    """Allocate on the call's own stream, so that the memory is not handed on before the call has used it."""
-    if stream is None:
-        return contextlib.nullcontext()
-    if not isinstance(stream, torch.cuda.Stream):
-        stream = torch.cuda.ExternalStream(int(stream), device=device)
-    return torch.cuda.stream(stream)
-
-
-def _empty(shape, dtype: torch.dtype, device: torch.device, stream) -> torch.Tensor:
-    """An output or workspace of a call on `stream` (None: the current one)."""
-    if stream is None or device.type != "cuda":
-        return torch.empty(shape, dtype=dtype, device=device)
-    with torch.cuda.device(device), _using(stream, device):
-        return torch.empty(shape, dtype=dtype, device=device)
+def _on_stream(stream, device):
+    """A call's stream as an integer, and the context to allocate its outputs in: memory must not be handed on
+    from the current stream's pool to another stream's call."""
+    if isinstance(stream, torch.cuda.Stream):
+        return stream.cuda_stream, torch.cuda.stream(stream)
+    return int(stream), torch.cuda.stream(torch.cuda.ExternalStream(int(stream), device=device))
 
 
 def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens_q: Optional[torch.Tensor] = None,
@@ -424,14 +385,14 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     cu_seqlens_k where a sequence has other keys than queries (a cached context in front).  Returns out, like q;
     rows that no sequence holds are not written.  softmax_scale defaults to D ** -0.5.  Spans outside the tensors
     are reported by get_error(), or raised here with check=True."""
-    if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
-    if softmax_scale is None:
-        softmax_scale = q.shape[-1] ** -0.5 if q.dim() and q.shape[-1] else 1.0
-    buf, d, dev = _pack("prompt_attention", (q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse), None)
-    call = lib().kvq_prompt_attention
-    _run("prompt_attention", lambda st: call(*d, 1 if causal else 0, softmax_scale, st), stream, check, dev)
-    return out
+    call = _calls().prompt_attention
+    if stream is None:
+        return _done("prompt_attention", call(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, causal, softmax_scale, None),
+                     check)
+    st, where = _on_stream(stream, q.device)
+    with where:
+        return _done("prompt_attention", call(q, k, v, cu_seqlens_q, cu_seqlens_k, out, lse, causal, softmax_scale, st),
+                     check)
 
 
 def shared_prefix_attention_workspace(batch: int, n_q: int, n_kv: int, dim: int, prefix_len: int,
@@ -454,41 +415,30 @@ def shared_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     q [B, Nq, D]; rows with seq_lens -1 are not written.  The workspace is allocated when not given (uint8,
     shared_prefix_attention_workspace() bytes, one per call that may run at the same time).  Bad pages and lengths
     are reported by get_error(), or raised here with check=True."""
-    if out is None:
-        out = _empty(q.shape, q.dtype, q.device, stream)
-    if softmax_scale is None:
-        softmax_scale = q.shape[-1] ** -0.5 if q.dim() and q.shape[-1] else 1.0
-    L = lib()
-    prefix_len = int(prefix_len)
-    if workspace is None and q.dim() == 3 and k_cache.dim() == 4 and block_table.dim() == 2:
-        need = L.kvq_shared_prefix_attention_workspace(q.shape[0], q.shape[1], k_cache.shape[2], q.shape[2], prefix_len,
-                                                       block_table.shape[1] * k_cache.shape[1])
-        if need > 0:
-            workspace = _empty((need,), torch.uint8, q.device, stream)
-    buf, d, dev = _pack("shared_prefix_attention", (q, k_cache, v_cache, block_table, seq_lens, prefix_table, scale_k,
-                                                    scale_v, offset_k, offset_v, out, lse, workspace), None)
-    call = L.kvq_shared_prefix_attention
-    _run("shared_prefix_attention", lambda st: call(*d[:6], prefix_len, *d[6:12], softmax_scale, d[12], st), stream,
-         check, dev)
-    return out
+    call = _calls().shared_prefix_attention
+    if stream is None:
+        return _done("shared_prefix_attention",
+                     call(q, k_cache, v_cache, block_table, seq_lens, prefix_table, prefix_len, scale_k, scale_v, offset_k,
+                          offset_v, out, lse, softmax_scale, workspace, None), check)
+    st, where = _on_stream(stream, q.device)
+    with where:
+        return _done("shared_prefix_attention",
+                     call(q, k_cache, v_cache, block_table, seq_lens, prefix_table, prefix_len, scale_k, scale_v, offset_k,
+                          offset_v, out, lse, softmax_scale, workspace, st), check)
 
 
 def copy_pages(caches: Sequence[torch.Tensor], src: torch.Tensor, dst: torch.Tensor, stream=None,
                check: bool = False) -> None:
     """In every cache [num_pages, ...], page dst[i] = page src[i] (see kvq_copy_pages); pairs with a -1 are
     skipped.  Pages out of range are reported by get_error(), or raised here with check=True."""
-    caches = list(caches)
-    buf, d, dev = _pack("copy_pages", (*caches, src, dst), None)
-    call = lib().kvq_copy_pages
-    _run("copy_pages", lambda st: call(d[0], len(caches), d[-2], d[-1], st), stream, check, dev)
+    _done("copy_pages", _calls().copy_pages(caches, src, dst, None if stream is None else _stream(stream)), check)
 
 
 def free_pages(block_table: torch.Tensor, seq_lens: torch.Tensor, ref_count: torch.Tensor, rows: torch.Tensor,
                block_size: int, stream=None, check: bool = False) -> None:
     """Give up the pages of the named rows (see kvq_free_pages): counts down by one, entries -1, lengths 0."""
-    buf, d, dev = _pack("free_pages", (block_table, seq_lens, ref_count, rows), None)
-    call = lib().kvq_free_pages
-    _run("free_pages", lambda st: call(*d, int(block_size), st), stream, check, dev)
+    _done("free_pages", _calls().free_pages(block_table, seq_lens, ref_count, rows, block_size,
+                                            None if stream is None else _stream(stream)), check)
 
 
 def fork_pages(caches: Sequence[torch.Tensor], block_table: torch.Tensor, seq_lens: torch.Tensor,
@@ -498,13 +448,14 @@ def fork_pages(caches: Sequence[torch.Tensor], block_table: torch.Tensor, seq_le
     partly filled last page is copied into the lowest free page.  Returns fresh, int32: that page for each child,
     -1 where nothing had to be copied, -2 for a child left empty (bits FAULT_NO_PAGE or FAULT_SLOT_RANGE, reported
     by get_error(), or raised here with check=True)."""
-    caches = list(caches)
-    if fresh is None:
-        fresh = _empty(children.shape, torch.int32, children.device, stream)
-    buf, d, dev = _pack("fork_pages", (*caches, block_table, seq_lens, ref_count, parents, children, fresh), None)
-    call = lib().kvq_fork_pages
-    _run("fork_pages", lambda st: call(d[0], len(caches), *d[-6:-1], int(block_size), d[-1], st), stream, check, dev)
-    return fresh
+    call = _calls().fork_pages
+    if stream is None:
+        return _done("fork_pages", call(caches, block_table, seq_lens, ref_count, parents, children, block_size, fresh,
+                                        None), check)
+    st, where = _on_stream(stream, children.device)
+    with where:
+        return _done("fork_pages", call(caches, block_table, seq_lens, ref_count, parents, children, block_size, fresh,
+                                        st), check)
 
 
 def compact_pages(caches: Sequence[torch.Tensor], block_table: torch.Tensor, ref_count: torch.Tensor,
@@ -514,17 +465,12 @@ def compact_pages(caches: Sequence[torch.Tensor], block_table: torch.Tensor, ref
     """Move the pages in use to the lowest page numbers, in every cache (see kvq_compact_pages).  Returns
     (new_table, new_ref_count, page_map), allocated when not given; new_table and new_ref_count may be the old
     ones, else those are left as they are."""
-    caches = list(caches)
-    if new_table is None:
-        new_table = _empty(block_table.shape, torch.int32, block_table.device, stream)
-    if new_ref_count is None:
-        new_ref_count = _empty(ref_count.shape, torch.int32, ref_count.device, stream)
-    if page_map is None:
-        page_map = _empty(ref_count.shape, torch.int32, ref_count.device, stream)
-    buf, d, dev = _pack("compact_pages", (*caches, block_table, ref_count, new_table, new_ref_count, page_map), None)
-    call = lib().kvq_compact_pages
-    _run("compact_pages", lambda st: call(d[0], len(caches), *d[-5:], st), stream, check, dev)
-    return new_table, new_ref_count, page_map
+    call = _calls().compact_pages
+    if stream is None:
+        return _done("compact_pages", call(caches, block_table, ref_count, new_table, new_ref_count, page_map, None), check)
+    st, where = _on_stream(stream, ref_count.device)
+    with where:
+        return _done("compact_pages", call(caches, block_table, ref_count, new_table, new_ref_count, page_map, st), check)
 
 
 # ---------------------------------------------------------------------------

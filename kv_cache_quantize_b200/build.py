@@ -1,4 +1,5 @@
-"""Build libkvq.so, the sm_100a CUDA library behind include/kvq.h.
+"""Build libkvq.so, the sm_100a CUDA library behind include/kvq.h, and _calls.so,
+the extension module that passes torch tensors to its attention and page calls.
 
 nvcc cross-compiles for sm_100a without a GPU.  -fmad=false keeps every
 binary32 multiply and add separately rounded (the kernels also use the
@@ -7,14 +8,19 @@ library only needs the driver.
 """
 import os
 import re
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libkvq.so")
 OBJ = os.path.join(HERE, "_build")
+CALLS = os.path.join(HERE, "_calls.so")
+CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
+CXX = os.environ.get("CXX", "g++")
 SOURCES = [os.path.join(CSRC, f) for f in ("kvq.cu", "attention.cu", "pages.cu")]
 NVCC = os.environ.get("NVCC", "nvcc")
 FLAGS = ["-gencode", "arch=compute_100a,code=sm_100a", "-lineinfo", "-O3", "-std=c++17", "-fmad=false",
@@ -41,7 +47,19 @@ def _stale(target, deps) -> bool:
 
 
 def needs_build() -> bool:
-    return _stale(LIB, {os.path.abspath(__file__)}.union(*(_deps(s) for s in SOURCES)))
+    here = {os.path.abspath(__file__)}
+    return _stale(LIB, here.union(*(_deps(s) for s in SOURCES))) or _stale(CALLS, here | _deps(CALLS_SOURCE))
+
+
+def _calls_command(out):
+    import torch
+    from torch.utils import cpp_extension
+    cuda = os.path.join(os.path.dirname(os.path.dirname(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")), "include")
+    include = [sysconfig.get_paths()["include"], *cpp_extension.include_paths(), cuda, os.path.join(ROOT, "include")]
+    return [CXX, "-O2", "-std=c++17", "-fPIC", "-shared", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            *("-isystem" + p for p in include), "-o", out, CALLS_SOURCE,
+            "-L" + os.path.join(os.path.dirname(torch.__file__), "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            "-L" + HERE, "-l:libkvq.so", "-Wl,-rpath,$ORIGIN"]
 
 
 def build(force: bool = False, verbose: bool = False) -> str:
@@ -63,6 +81,9 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(o + tag, o)
     subprocess.run([NVCC, *FLAGS, "-shared", "-o", LIB + tag, *objects], check=True)
     os.replace(LIB + tag, LIB)
+    if force or _stale(CALLS, _deps(CALLS_SOURCE) | {os.path.abspath(__file__)}):
+        subprocess.run(_calls_command(CALLS + tag), check=True)
+        os.replace(CALLS + tag, CALLS)
     return LIB
 
 

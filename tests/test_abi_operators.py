@@ -229,12 +229,28 @@ def test_binding_refuses_host_tensors_and_other_types(L):
         kvq.free_pages([[1, 2]], cu, cu, cu, 16)
 
 
-def test_descriptors_of_the_packed_form_are_those_of_desc():
-    """The packed descriptors carry the same fields, field for field."""
-    for x in (torch.zeros((3, 0), dtype=I8), torch.empty((0,) * 8, dtype=I64)):
-        buf, at, dev = kvq._pack("x", (x, None, x), None)
-        assert at[1] is None and dev is None
-        for a in (at[0], at[2]):
-            assert bytes(kvq.KvqTensor.from_address(a)) == bytes(kvq.desc(x))
+def test_descriptors_of_the_extension_are_those_of_desc():
+    """Field for field the ones of the ctypes binding."""
+    for x in (torch.zeros((3, 0), dtype=I8), torch.empty((0,) * 8, dtype=I64), torch.empty((0, 2), dtype=torch.float8_e8m0fnu)):
+        assert kvq._calls().descriptor(x) == bytes(kvq.desc(x))
+    for dt in kvq._DTYPES:
+        assert kvq._calls().descriptor(torch.empty((0,), dtype=dt)) == bytes(kvq.desc(torch.empty((0,), dtype=dt)))
     with pytest.raises(ValueError):
-        kvq._pack("x", (torch.empty((0,) * 9),), None)
+        kvq._calls().descriptor(torch.empty((0,) * 9))
+
+
+def test_extension_refuses_wrong_arguments():
+    c = kvq._calls()
+    e = torch.empty((0, 2, 64), dtype=BF)
+    with pytest.raises(TypeError):
+        c.prompt_attention(e, e)
+    with pytest.raises(TypeError):
+        kvq.prompt_attention(e, e, e, softmax_scale="x")
+    with pytest.raises(TypeError):
+        kvq.copy_pages([None], e, e)
+    with pytest.raises(TypeError):
+        kvq.copy_pages(3, e, e)
+    with pytest.raises(TypeError):
+        kvq.free_pages(e, e, e, e, "sixteen")
+    with pytest.raises(kvq.KvqError):
+        kvq.prompt_attention(e, e, e)
