@@ -80,7 +80,7 @@ kvq_status run_copy(PageCopyArgs& a, cudaStream_t s) {
         a.units += (c.bytes + a.chunk - 1) / a.chunk;
     }
     if (a.units == 0) a.units = 1, a.n_caches = 0;
-    const int64_t need = a.n_pairs * a.units;
+    const int64_t need = a.n_pairs * a.units;                   // units; a CTA takes every grid-th one
     auto go = [&](auto kernel) {
         return launched(launch(kernel, (unsigned)persistent_grid(kernel, PG_THREADS, need), PG_THREADS, 0, s, a));
     };
