@@ -113,6 +113,26 @@ int64_t shared_plan(int64_t B, int64_t Nq, int64_t Nkv, int64_t D, int64_t prefi
     return (p->own_stats + 2 * own) * 4;
 }
 
+// A cache [pages, block, Nkv, D] in boxes of up to 128 tokens of one page and
+// head: int8 rows as they are, 16-bit ones 64 values at a time with the 128-byte
+// swizzle.
+bool pages_map(CUtensorMap* m, int type, const void* base, const SharedArgs& a) {
+    PFN_cuTensorMapEncodeTiled_v12000 enc = tensor_map_encoder();
+    if (!enc) return false;
+    const bool i8 = type == ATT_I8;
+    const int64_t eb = i8 ? 1 : 2, row = (int64_t)a.Nkv * a.D * eb;
+    const cuuint64_t dims[4] = {(cuuint64_t)a.D, (cuuint64_t)a.Nkv, (cuuint64_t)a.block, (cuuint64_t)a.num_pages};
+    const cuuint64_t strides[3] = {(cuuint64_t)(a.D * eb), (cuuint64_t)row,
+                                   (cuuint64_t)(a.num_pages > 1 ? a.page_bytes : row * a.block)};
+    const cuuint32_t box[4] = {(cuuint32_t)(i8 ? a.D : 64), 1, (cuuint32_t)(a.block < SA_KEYS ? a.block : SA_KEYS), 1};
+    const cuuint32_t estr[4] = {1, 1, 1, 1};
+    return enc(m, i8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
+                     : type == ATT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16,
+               4, const_cast<void*>(base), dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+               i8 ? CU_TENSOR_MAP_SWIZZLE_NONE : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <int T, int C, int D>
 kvq_status run_shared(const SharedArgs& a, cudaStream_t s) {
     constexpr bool I8 = C == ATT_I8;
@@ -125,10 +145,14 @@ kvq_status run_shared(const SharedArgs& a, cudaStream_t s) {
     // at most one CTA per step that the lengths can ask for
     const int64_t steps = (int64_t)p.n_groups * a.Nkv * p.blocks +
                           (int64_t)a.B * a.Nkv * (((int64_t)a.cols * a.block + SA_KEYS - 1) / SA_KEYS);
-    auto kernel = shared_kernel<T, C, D>;
+    // TMA where a page holds 8, 16, 32 .. tokens: a swizzle repeats after 8 rows
+    const bool tma = a.block_shift >= 3 && a.num_pages > 0;
+    CUtensorMap mk = {}, mv = {};
+    if (tma && (!pages_map(&mk, C, a.k_cache, a) || !pages_map(&mv, C, a.v_cache, a))) return KVQ_ERR_CUDA;
+    auto kernel = tma ? shared_kernel<T, C, D, true> : shared_kernel<T, C, D, false>;
     constexpr uint32_t smem = sa_smem_bytes(D, I8);
     const int64_t ctas = persistent_grid(kernel, SA_THREADS, steps < SA_MAX_CTAS ? steps : SA_MAX_CTAS, smem);
-    if (steps > 0 && launch(kernel, (unsigned)ctas, SA_THREADS, smem, s, mq, mq1, a, p) != cudaSuccess) return KVQ_ERR_CUDA;
+    if (steps > 0 && launch(kernel, (unsigned)ctas, SA_THREADS, smem, s, mq, mq1, mk, mv, a, p) != cudaSuccess) return KVQ_ERR_CUDA;
     const int hblocks = (a.Nq + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
     return launched(launch(shared_join_kernel<T, C, D>, (unsigned)(a.B * hblocks), SJ_THREADS, 0, s, a, p, (int)ctas,
                            hblocks));

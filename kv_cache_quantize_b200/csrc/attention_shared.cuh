@@ -20,13 +20,18 @@
 // rows: both tiles then hold the same rows and take the steps in turn.
 //
 //   warps 0-3, 4-7   softmax of tile 0 and 1, a thread per row;
-//   warps 8-11       keys and values: 16-byte asynchronous copies through the
-//                    page lists, any page size; int8 codes are turned into f16
-//                    (exactly) on their way into the product's tiles;
+//   warps 8-11       int8 codes to f16 (exactly), from raw tiles into the
+//                    product's; over 16-bit caches, zeros in V's last rows
+//                    behind the keys;
 //   warp 12          issues tcgen05.mma;
 //   warp 13          cuts the work, and loads Q where it needs no scaling;
 //   warps 14, 15     scale Q over int8 caches, tile 0 and 1, for the next piece
 //                    while the tiles' last steps run.
+//
+// Pages of 8, 16, 32 .. tokens come by TMA, a box of up to 128 tokens of one
+// page (warp 13 over int8 caches, 14 over 16-bit ones).  Other page sizes come
+// by 16-byte asynchronous copies of warps 8-11, which cost those warps 790
+// cycles for a tile of 128 int8 keys, as much again as the conversion.
 //
 // int8 caches: value = (code - offset) * scale per channel.  q is multiplied
 // by the key scale in fp32, scaled by a power of two per row to f16's range
@@ -57,7 +62,7 @@ __host__ __device__ constexpr int sa_lag(bool i8) { return i8 ? 3 : 2; }
 __host__ __device__ constexpr uint32_t sa_tile_bytes(int D) { return 128u * (uint32_t)D * 2u; }
 __host__ __device__ constexpr uint32_t sa_smem_bytes(int D, bool i8) {
     return (2u + (uint32_t)sa_ring(i8)) * sa_tile_bytes(D) + (i8 ? (uint32_t)(sa_lag(i8) + 1) * sa_tile_bytes(D) / 2u : 0u) +
-           512u + SA_PAGES * 512u + 512u;          // + barriers and items, page numbers, exponents
+           768u + SA_PAGES * 512u + 512u;          // + barriers and items, places of keys, exponents
 }
 
 // the cost of a step: two tiles of rows, one tile (prefix), a request's own
@@ -131,9 +136,20 @@ __device__ __forceinline__ void i8x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
 __device__ __forceinline__ uint32_t k_pos(int s) { return s == 0 ? 0u : 2u * s - 1u; }
 __device__ __forceinline__ uint32_t v_pos(int s, int n) { return s == n - 1 ? 2u * n - 1u : 2u * s + 2u; }
 
-template <int T, int C, int D>
+// TMA load of box {x, y, z, w} of a cache [pages, block, Nkv, D]
+__device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t head, int32_t token,
+                                              int32_t page, uint64_t* bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(head), "r"(token), "r"(page), "r"(smem_u32(bar))
+        : "memory");
+}
+
+template <int T, int C, int D, bool TM>
 __global__ void __launch_bounds__(SA_THREADS, 1)
     shared_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_q1,
+                  const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
                   const __grid_constant__ SharedArgs a, const __grid_constant__ SharedPlan plan) {
     constexpr bool I8 = C == ATT_I8;
     constexpr int MT = I8 ? ATT_F16 : T;                     // type of the products
@@ -157,7 +173,11 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     uint64_t* item_empty = item_full + SA_ITEMS;
     uint64_t* kv_full = item_empty + SA_ITEMS;
     uint64_t* kv_empty = kv_full + NS;
-    uint64_t* page_bar = kv_empty + NS;
+    // raw_full: int8 tiles by TMA; over 16-bit caches the last V tiles of pieces, before their
+    // zeros, in turn (at most 3 of them are in a ring of 5)
+    uint64_t* raw_full = kv_empty + NS;
+    uint64_t* raw_empty = raw_full + 4;
+    uint64_t* page_bar = raw_empty + 4;
     uint64_t* drain = page_bar + 1;
     uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(drain + 1);
     volatile uint32_t* bad = reinterpret_cast<volatile uint32_t*>(tmem_slot + 2);      // [SA_BAD]
@@ -185,11 +205,15 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         }
         for (int i = 0; i < SA_ITEMS; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], HILO ? 14 : I8 ? 15 : 13);      // 8 softmax, 4 load and 0 to 2 Q warps, the MMA lane
+            mbar_init(&item_empty[i], HILO ? 14 : I8 ? 15 : TM ? 14 : 13);     // 8 softmax warps, 8-11, 12, and those of 14, 15 in use
         }
         for (int i = 0; i < NS; ++i) {
-            mbar_init(&kv_full[i], 128);
+            mbar_init(&kv_full[i], !I8 && TM ? 5 : 128);         // by TMA: the issuer and warps 8-11
             mbar_init(&kv_empty[i], 1);
+        }
+        for (int i = 0; i < 4; ++i) {
+            mbar_init(&raw_full[i], 1);
+            mbar_init(&raw_empty[i], 4);
         }
         mbar_init(page_bar, 128);
         mbar_init(drain, 1);
@@ -216,11 +240,81 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     const int64_t total = pre_cost + (int64_t)*s_blocks * a.Nkv * plan.cost_own;
     const int64_t width = (total + gridDim.x - 1) / gridDim.x;
 
+    // The K and V tiles of a piece by TMA, all lanes of one warp: a lane for
+    // each stretch of `box` tokens that lies in one page.  `tile_no` and
+    // `step_no` count over all pieces.
+    auto load_tiles = [&](int n, int own, int b0, int kh, int key0, int keys, uint32_t& tile_no, uint32_t& step_no,
+                          uint32_t& tails) -> bool {
+        constexpr int EB = I8 ? 1 : 2;
+        const int32_t* list = own ? a.table + (int64_t)b0 * a.table_stride : a.prefix_table;
+        const int box = min(a.block, SA_KEYS), pieces = SA_KEYS / box;
+        for (int q = 0; q < 2 * n; ++q, ++tile_no) {
+            // the order K0 K1 V0 K2 V1 ... V(n-1)
+            const bool is_v = q > 0 && ((q & 1) == 0 || q == 2 * n - 1);
+            const int s = q == 0 ? 0 : is_v ? (q == 2 * n - 1 ? n - 1 : (q - 2) / 2) : (q + 1) / 2;
+            const int t = s * SA_KEYS + lane * box;
+            const bool wanted = lane < pieces && t < keys;
+            int32_t page = -1;
+            if (wanted) page = __ldg(list + ((key0 + t) >> a.block_shift));
+            const bool there = (uint32_t)page < (uint32_t)a.num_pages;
+            const unsigned got = __ballot_sync(FULL_MASK, there), lost = __ballot_sync(FULL_MASK, wanted && !there);
+            const uint32_t st = I8 ? tile_no % NR : tile_no % NS, turn = I8 ? tile_no / NR : tile_no / NS;
+            if (!__all_sync(FULL_MASK, mbar_wait_ns(I8 ? &raw_empty[st] : &kv_empty[st], (turn & 1u) ^ 1u, SA_WAIT_NS))) return false;
+            uint8_t* tile = I8 ? raw_s + st * (TILE / 2) : kv_s + st * TILE;
+            if (lost) {
+                // pages that are not there: their keys are marked, and their rows of V hold zeros
+                if (!is_v) {
+                    if (lane < 4) {
+                        uint32_t have = 0;
+                        for (int k = 0; k < 32; ++k) have |= ((got >> ((32 * lane + k) / box)) & 1u) << k;
+                        key_ok[(step_no % SA_BAD) * 4 + lane] = have;
+                    }
+                    if (lane == 0) {
+                        bad[step_no % SA_BAD] = step_no + 1;
+                        raise_fault(FAULT_SLOT_RANGE);
+                    }
+                } else if (!I8) {
+                    for (int k = lane; k < SA_KEYS * 8 * PANELS; k += 32)
+                        if ((lost >> ((k >> 3) % SA_KEYS / box)) & 1u)
+                            *reinterpret_cast<uint4*>(tile + (k >> 3) / SA_KEYS * PANEL + (k >> 3) % SA_KEYS * 128 + (k & 7) * 16) =
+                                make_uint4(0u, 0u, 0u, 0u);
+                    fence_proxy_async_smem();
+                }
+                __syncwarp();
+            }
+            if (!is_v) ++step_no;
+            const bool tail = !I8 && is_v && s == n - 1 && keys < n * SA_KEYS;
+            uint64_t* bar = I8 ? &raw_full[st] : tail ? &raw_full[tails++ % 4] : &kv_full[st];
+            if (lane == 0) {
+                mbar_arrive_expect_tx(bar, (uint32_t)__popc(got) * box * D * EB);
+                if (tail) mbar_arrive(&kv_full[st]);
+            }
+            __syncwarp();
+            if (there) {
+                const CUtensorMap* map = is_v ? &tm_v : &tm_k;
+                const int32_t in = (key0 + t) & (a.block - 1);
+                if (I8) {
+                    tma_load_page(smem_u32(tile) + lane * box * D, map, 0, kh, in, page, bar);
+                } else {
+                    for (int p = 0; p < PANELS; ++p)
+                        tma_load_page(smem_u32(tile) + p * PANEL + lane * box * 128, map, 64 * p, kh, in, page, bar);
+                }
+            }
+        }
+        return true;
+    };
+    // no load may still be in flight when the CTA exits
+    auto drain_tiles = [&](uint32_t tile_no) {
+        constexpr uint32_t R = I8 ? NR : NS;
+        for (uint32_t k = tile_no > R ? tile_no - R : 0; k < tile_no; ++k)
+            mbar_wait_ns(I8 ? &raw_full[k % R] : &kv_full[k % R], (k / R) & 1u, SA_WAIT_NS);
+    };
+
     // 512 threads x 128 registers at launch, split 256 x 160 + 128 x 120 + 128 x 72
     if (warp == 13) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---------------- work, and Q where TMA can bring it ----------------
-        uint32_t n_item = 0, q_n[2] = {0, 0};
+        uint32_t n_item = 0, q_n[2] = {0, 0}, tile_no = 0, step_no = 0, tails = 0;
         const int64_t hi = min((int64_t)(blockIdx.x + 1) * width, total);
         int64_t at = (int64_t)blockIdx.x * width;
         int cb = 0;                                          // cursor over the requests
@@ -331,7 +425,9 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 }
             }
             dead = __shfl_sync(FULL_MASK, dead, 0);
+            if (I8 && TM) dead = !load_tiles(w.steps, w.own, w.b0, w.kh, w.key0, w.keys, tile_no, step_no, tails);
         }
+        if (I8 && TM) drain_tiles(tile_no);
         if (!I8 && lane == 0)
             for (int i = 0; i < 2; ++i)
                 if (q_n[i] > 0) mbar_wait_ns(&q_full[i], (q_n[i] - 1) & 1u, SA_WAIT_NS);
@@ -412,6 +508,20 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         }
     } else if (warp >= 14) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+        if (!I8 && TM && warp == 14) {
+            // ---------------- K and V tiles, 16-bit ----------------
+            uint32_t tile_no = 0, step_no = 0, tails = 0;
+            for (uint32_t n_item = 0;; ++n_item) {
+                const uint32_t slot = n_item % SA_ITEMS;
+                if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
+                const int n = items[slot].steps, own = items[slot].own, b0 = items[slot].b0, kh = items[slot].kh;
+                const int key0 = items[slot].key0, keys = items[slot].keys;
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&item_empty[slot]);
+                if (n < 0 || !load_tiles(n, own, b0, kh, key0, keys, tile_no, step_no, tails)) break;
+            }
+            drain_tiles(tile_no);
+        }
         // ---------------- Q times the key scale ----------------
         if (I8 && !(HILO && warp == 15)) {
             constexpr int LPR = D / 16;                      // lanes of a row, 16 channels each
@@ -516,11 +626,13 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         constexpr int PASSES = 128 / RP;
         const int ch = p % CH, r0 = p / CH;
         const uint32_t row_units = (uint32_t)(a.Nkv * (D * EB / 64)), page_units = (uint32_t)(a.page_bytes / 64);
-        uint32_t issued = 0, done = 0, block_no = 0;
+        uint32_t issued = 0, done = 0, block_no = 0, tails_seen = 0;
         bool ok = true;
         auto finish = [&]() {
             if (I8) {
                 // this thread's own copies have arrived: codes to f16
+                if (TM) ok = __all_sync(FULL_MASK, mbar_wait_ns(&raw_full[done % NR], (done / NR) & 1u, SA_WAIT_NS));
+                if (!ok) return;
                 ok = __all_sync(FULL_MASK, mbar_wait_ns(&kv_empty[done % NS], ((done / NS) & 1u) ^ 1u, SA_WAIT_NS));
                 if (!ok) return;
                 const uint8_t* src = raw_s + (done % NR) * (TILE / 2) + p * 16;
@@ -530,6 +642,10 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 uint4 raw[PASSES];
 #pragma unroll
                 for (int k = 0; k < PASSES; ++k) raw[k] = *reinterpret_cast<const uint4*>(src + k * 2048);
+                if (TM) {
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&raw_empty[done % NR]);
+                }
 #pragma unroll
                 for (int k = 0; k < PASSES; ++k) {
                     const uint4 w = raw[k];
@@ -557,6 +673,35 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
             if (n < 0) break;
+            if (TM) {
+                uint32_t tails = tails_seen;
+                for (int q = 0; q < 2 * n && ok; ++q) {
+                    if (I8) {
+                        finish();
+                        continue;
+                    }
+                    const uint32_t st = done % NS;
+                    ok = __all_sync(FULL_MASK, mbar_wait_ns(&kv_empty[st], ((done / NS) & 1u) ^ 1u, SA_WAIT_NS));
+                    if (!ok) break;
+                    if (q == 2 * n - 1 && keys < n * SA_KEYS) {
+                        // V's rows behind the last key, once they are there
+                        ok = __all_sync(FULL_MASK, mbar_wait_ns(&raw_full[tails % 4], (tails / 4) & 1u, SA_WAIT_NS));
+                        ++tails;
+                        if (!ok) break;
+                        const int first = keys - (n - 1) * SA_KEYS;
+                        for (int k = first * 8 + p; k < SA_KEYS * 8; k += 128)
+#pragma unroll
+                            for (int z = 0; z < PANELS; ++z)
+                                *reinterpret_cast<uint4*>(kv_s + st * TILE + z * PANEL + k * 16) = make_uint4(0u, 0u, 0u, 0u);
+                        fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&kv_full[st]);
+                    ++done;
+                }
+                tails_seen = tails;
+                continue;
+            }
             const int32_t* list = own ? a.table + (int64_t)b0 * a.table_stride : a.prefix_table;
             const int64_t head = (int64_t)kh * D * EB + ch * 16;
             // thread p looks up the place of key p of each step, one step ahead, in units of 64 bytes from the
@@ -618,7 +763,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             }
         }
         cp_async_wait<0>();
-        while (ok && done < issued) finish();
+        while (!TM && ok && done < issued) finish();
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 160;");
         // ---------------- softmax and partial results ----------------
