@@ -93,14 +93,16 @@ int64_t shared_plan(int64_t B, int64_t Nq, int64_t Nkv, int64_t D, int64_t prefi
     const int64_t G = Nq / Nkv, tok = 128 / G;
     auto area = [&](int64_t group, int64_t* slots, int64_t* rows) {
         *slots = prefix_len > 0 ? ((B + group - 1) / group) * Nkv + SA_MAX_CTAS : 0;
-        *rows = (B < tok ? B : tok) * G;
+        // several groups: whole tiles; one group: its rows, four times where they are few
+        *rows = B > tok ? 128 : B * G <= 32 ? 4 * B * G : B * G;
         return *slots * 2 * *rows;
     };
     int64_t slots, rows;
     const int64_t group = hilo ? tok : 2 * tok;
     const int64_t pre = area(tok, &slots, &rows);                   // rows of the prefix slots, the larger form
     area(group, &slots, &rows);
-    const int64_t own = (B * Nkv + SA_MAX_CTAS) * 2 * G;
+    p->own_rows = (int32_t)(G <= 32 ? 4 * G : G);
+    const int64_t own = (B * Nkv + SA_MAX_CTAS) * 2 * p->own_rows;
     p->group = (int32_t)group;
     p->n_groups = (int32_t)((B + group - 1) / group);
     p->blocks = (int32_t)((prefix_len + SA_KEYS - 1) / SA_KEYS);
@@ -140,7 +142,7 @@ kvq_status run_shared(const SharedArgs& a, cudaStream_t s) {
     shared_plan(a.B, a.Nq, a.Nkv, D, a.prefix_len, I8 && T == ATT_F16, &p);
     p.cost_own = I8 ? SA_COST_OWN8 : SA_COST_OWN16;
     CUtensorMap mq = {}, mq1 = {};
-    if (!I8 && (!rows_map(&mq, T, a.q, a.B, a.Nq, D, a.G, 128 / a.G) || !rows_map(&mq1, T, a.q, a.B, a.Nq, D, a.G, 1)))
+    if (!I8 && (!rows_map(&mq, T, a.q, a.B, a.Nq, D, a.G, 128 / a.G) || !rows_map(&mq1, T, a.q, a.B, a.Nq, D, a.G, a.G <= 32 ? 32 / a.G : 1)))
         return KVQ_ERR_CUDA;
     // at most one CTA per step that the lengths can ask for
     const int64_t steps = (int64_t)p.n_groups * a.Nkv * p.blocks +

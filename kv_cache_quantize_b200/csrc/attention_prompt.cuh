@@ -381,7 +381,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 const float bm = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
                 // the row's own reference moves only when its maximum has outgrown it
                 // (or is NaN, which then stays)
-                const bool grow = !(__fmul_rn(__fsub_rn(bm, m), c) <= PA_SLACK) && bm != -INFINITY;
+                const bool grow = live && !(__fmul_rn(__fsub_rn(bm, m), c) <= PA_SLACK) && bm != -INFINITY;
                 if (j == 0) {
                     m = bm;
                 } else if (__any_sync(FULL_MASK, grow)) {

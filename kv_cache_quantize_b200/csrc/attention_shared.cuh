@@ -18,6 +18,11 @@
 // Two query tiles are in flight per CTA, one in its softmax while the tensor
 // core works on the other.  A group of up to 128 rows has only one tile of
 // rows: both tiles then hold the same rows and take the steps in turn.
+// A group of up to 32 rows (a request's own keys, a small batch) would leave
+// one warp of each tile to go through 128 keys alone, some 2600 cycles: its
+// rows stand four times in the tile, at lanes 0, 32, 64 and 96, and the warp of
+// each copy takes 32 of the step's keys, its weights of the others being zero.
+// The four are pieces of their own for the join.
 //
 //   warps 0-3, 4-7   softmax of tile 0 and 1, a thread per row;
 //   warps 8-11       int8 codes to f16 (exactly), from raw tiles into the
@@ -26,7 +31,9 @@
 //   warp 12          issues tcgen05.mma;
 //   warp 13          cuts the work, and loads Q where it needs no scaling;
 //   warps 14, 15     scale Q over int8 caches, tile 0 and 1, for the next piece
-//                    while the tiles' last steps run.
+//                    while the tiles' last steps run (pieces of up to 32 rows;
+//                    the softmax warps do it for larger ones: one warp alone
+//                    took 29000 cycles for 128 rows).
 //
 // Pages of 8, 16, 32 .. tokens come by TMA, a box of up to 128 tokens of one
 // page (warp 13 over int8 caches, 14 over 16-bit ones).  Other page sizes come
@@ -76,6 +83,7 @@ struct SharedPlan {
     int32_t cost_own;
     int32_t last_alt;        // the last group of requests has one tile of rows
     int32_t tile_rows;       // rows of a tile in a prefix slot
+    int32_t own_rows;        // and in an own slot
     int64_t own_area;        // floats before the own slots
     int64_t stats_area;      // floats before the (maximum, sum) pairs of the prefix slots; own_stats behind
     int64_t own_stats;
@@ -86,6 +94,7 @@ struct SharedItem {
     int32_t steps;           // -1: no more work
     int32_t alt;             // both tiles hold the same rows and take the steps in turn
     int32_t own;             // a request's own keys
+    int32_t narrow;          // up to 32 rows, four times in each tile
     int32_t b0, nreq;        // requests
     int32_t kh;
     int32_t key0, keys;      // first key of the list, keys in all
@@ -197,7 +206,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     }
     if (threadIdx.x == 0) {
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], I8 ? 32 : 1);
+            mbar_init(&q_full[i], I8 ? 4 : 1);
             mbar_init(&q_empty[i], 1);
             mbar_init(&s_full[i], 1);
             mbar_init(&p_ready[i], 128);
@@ -310,6 +319,83 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             mbar_wait_ns(I8 ? &raw_full[k % R] : &kv_full[k % R], (k / R) & 1u, SA_WAIT_NS);
     };
 
+    // Rows [begin, end) of tile i's Q (requests from b0 on) times the key scale,
+    // by one warp: LPR lanes share a row, 16 channels each.
+    auto scale_rows = [&](int i, int begin, int end, int b0, int kh, int own, bool copies, uint32_t parity) {
+        constexpr int LPR = D / 16, RPP = 32 / LPR;          // rows of a pass
+        const int sub = lane % LPR, c16 = sub * 16;
+        float sc[16];
+        const float4* sk = reinterpret_cast<const float4*>(a.scale_k + kh * D + c16);
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const float4 e = __ldg(sk + z);
+            sc[4 * z] = e.x;
+            sc[4 * z + 1] = e.y;
+            sc[4 * z + 2] = e.z;
+            sc[4 * z + 3] = e.w;
+        }
+        uint4 e[4][2];
+#pragma unroll 1
+        for (int r0 = begin; r0 < end; r0 += 4 * RPP) {
+            // four passes' loads are in flight together
+#pragma unroll
+            for (int z = 0; z < 4; ++z) {
+                const int lr = r0 + z * RPP + lane / LPR;
+                const int b = b0 + (own ? 0 : lr / a.G), h = kh * a.G + (own ? lr : lr % a.G);
+                const uint4* q = reinterpret_cast<const uint4*>(a.q.base + ((int64_t)b * a.q.tok + h * a.q.head + c16) * 2);
+                e[z][0] = lr < end ? __ldg(q) : make_uint4(0u, 0u, 0u, 0u);
+                e[z][1] = lr < end ? __ldg(q + 1) : make_uint4(0u, 0u, 0u, 0u);
+            }
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                if (r0 + u * RPP >= end) break;
+                const int lr = r0 + u * RPP + lane / LPR;
+                const bool live = lr < end;
+                const uint4 e0 = e[u][0], e1 = e[u][1];
+                const uint32_t ew[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
+                float x[16], top = 0.0f;
+#pragma unroll
+                for (int z = 0; z < 8; ++z) {
+                    float lo, hi;
+                    unpack2<T>(ew[z], lo, hi);
+                    x[2 * z] = __fmul_rn(lo, sc[2 * z]);
+                    x[2 * z + 1] = __fmul_rn(hi, sc[2 * z + 1]);
+                    top = fmaxf(top, fmaxf(fabsf(x[2 * z]), fabsf(x[2 * z + 1])));
+                }
+#pragma unroll
+                for (int d = 1; d < LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
+                // the power of two below the row's largest; 127 (times one) where there is none
+                uint32_t ex = __float_as_uint(top) >> 23;
+                if (ex == 0 || ex >= 254) ex = 127;
+                const float down = __uint_as_float((254u - ex) << 23);
+                if (live) {
+                    if (sub == 0) q_exp[(parity * 2 + i) * 128 + lr] = (uint8_t)ex;
+                    uint32_t hi[8], lo[8];
+#pragma unroll
+                    for (int z = 0; z < 8; ++z) {
+                        const float a0 = __fmul_rn(x[2 * z], down), a1 = __fmul_rn(x[2 * z + 1], down);
+                        hi[z] = pack2<ATT_F16>(a0, a1);
+                        if (HILO) {
+                            float h0, h1;
+                            unpack2<ATT_F16>(hi[z], h0, h1);
+                            lo[z] = pack2<ATT_F16>(__fsub_rn(a0, h0), __fsub_rn(a1, h1));
+                        }
+                    }
+                    for (int r = lr; r < (copies ? 128 : lr + 1); r += 32) {
+                        uint8_t* row = q_s + (HILO ? 0 : i) * TILE + (sub / 4) * PANEL + r * 128;
+                        const int p0 = ((2 * (sub & 3)) ^ (r & 7)) << 4, p1 = ((2 * (sub & 3) + 1) ^ (r & 7)) << 4;
+                        *reinterpret_cast<uint4*>(row + p0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        *reinterpret_cast<uint4*>(row + p1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
+                        if (HILO) {
+                            *reinterpret_cast<uint4*>(row + TILE + p0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                            *reinterpret_cast<uint4*>(row + TILE + p1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
+                        }
+                    }
+                }
+            }
+        }
+    };
+
     // 512 threads x 128 registers at launch, split 256 x 160 + 128 x 120 + 128 x 72
     if (warp == 13) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
@@ -385,6 +471,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                     w.steps = (int32_t)(s1 - s0);
                     w.key0 = (int32_t)s0 * SA_KEYS;
                     w.keys = min(len - w.key0, w.steps * SA_KEYS);
+                    w.narrow = w.alt && w.nreq * a.G <= 32;
                     w.slot = g + (int)blockIdx.x;
                 }
             }
@@ -395,6 +482,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 o.steps = w.steps;
                 o.alt = w.alt;
                 o.own = w.own;
+                o.narrow = w.narrow;
                 o.b0 = w.b0;
                 o.nreq = w.nreq;
                 o.kh = w.kh;
@@ -414,13 +502,16 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                         break;
                     }
                     ++q_n[i];
-                    mbar_arrive_expect_tx(&q_full[i], (uint32_t)(w.own ? a.G : TOK * a.G) * 128u * PANELS);
+                    // tm_q: a whole tile of requests; tm_q1: as many as 32 rows hold, or one
+                    const int few = a.G <= 32 ? 32 / a.G : 1;
+                    const bool one = w.narrow || w.own;
+                    const int copies = w.narrow ? 4 : 1;
+                    mbar_arrive_expect_tx(&q_full[i], (uint32_t)(one ? few * copies : TOK) * a.G * 128u * PANELS);
                     for (int p = 0; p < PANELS; ++p) {
                         uint8_t* dst = q_s + i * TILE + p * PANEL;
-                        // a request's own rows: lanes 32 .. in tile 1, so that the two tiles' softmax
-                        // warps sit on different schedulers
-                        if (w.own) tma_load_3d(dst + (i && a.G <= 96 ? 32 * 128 : 0), &tm_q1, 64 * p, w.kh * a.G, w.b0, &q_full[i]);
-                        else tma_load_3d(dst, &tm_q, 64 * p, w.kh * a.G, w.b0 + (w.alt ? 0 : i * TOK), &q_full[i]);
+                        if (!one) tma_load_3d(dst, &tm_q, 64 * p, w.kh * a.G, w.b0 + (w.alt ? 0 : i * TOK), &q_full[i]);
+                        for (int z = 0; one && z < copies; ++z)
+                            tma_load_3d(dst + z * 32 * 128, &tm_q1, 64 * p, w.kh * a.G, w.b0, &q_full[i]);
                     }
                 }
             }
@@ -524,16 +615,13 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         }
         // ---------------- Q times the key scale ----------------
         if (I8 && !(HILO && warp == 15)) {
-            constexpr int LPR = D / 16;                      // lanes of a row, 16 channels each
-            constexpr int RPP = 32 / LPR;                    // rows of a pass
             const int i = warp - 14;
-            const int sub = lane % LPR, c16 = sub * 16;
             uint32_t used = 0;
             for (uint32_t n_item = 0;; ++n_item) {
                 const uint32_t slot = n_item % SA_ITEMS;
                 if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
                 const int steps = items[slot].steps, alt = items[slot].alt, own = items[slot].own;
-                const int nreq = items[slot].nreq, kh = items[slot].kh;
+                const int nreq = items[slot].nreq, kh = items[slot].kh, narrow = items[slot].narrow;
                 const int b0 = items[slot].b0 + (alt ? 0 : i * TOK);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&item_empty[slot]);
@@ -541,79 +629,13 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 if (i && alt && steps == 1) continue;
                 if (!__all_sync(FULL_MASK, mbar_wait_ns(&q_empty[i], (used & 1u) ^ 1u, SA_WAIT_NS))) break;
                 const int rows = (alt ? nreq : min(nreq - i * TOK, TOK)) * a.G;
-                const int r_at = own && i && !HILO && a.G <= 96 ? 32 : 0;
-                float sc[16];
-                const float4* sk = reinterpret_cast<const float4*>(a.scale_k + kh * D + c16);
-#pragma unroll
-                for (int z = 0; z < 4; ++z) {
-                    const float4 e = __ldg(sk + z);
-                    sc[4 * z] = e.x;
-                    sc[4 * z + 1] = e.y;
-                    sc[4 * z + 2] = e.z;
-                    sc[4 * z + 3] = e.w;
-                }
-                uint4 e[4][2];
-#pragma unroll 1
-                for (int r0 = 0; r0 < rows; r0 += 4 * RPP) {
-                    // four passes' loads are in flight together
-#pragma unroll
-                    for (int z = 0; z < 4; ++z) {
-                        const int lr = r0 + z * RPP + lane / LPR;
-                        const int b = b0 + (own ? 0 : lr / a.G), h = kh * a.G + (own ? lr : lr % a.G);
-                        const uint4* q = reinterpret_cast<const uint4*>(a.q.base + ((int64_t)b * a.q.tok + h * a.q.head + c16) * 2);
-                        e[z][0] = lr < rows ? __ldg(q) : make_uint4(0u, 0u, 0u, 0u);
-                        e[z][1] = lr < rows ? __ldg(q + 1) : make_uint4(0u, 0u, 0u, 0u);
-                    }
-#pragma unroll
-                    for (int u = 0; u < 4; ++u) {
-                        if (r0 + u * RPP >= rows) break;
-                        const int lr = r0 + u * RPP + lane / LPR;
-                        const bool live = lr < rows;
-                        const uint4 e0 = e[u][0], e1 = e[u][1];
-                        const uint32_t ew[8] = {e0.x, e0.y, e0.z, e0.w, e1.x, e1.y, e1.z, e1.w};
-                        float x[16], top = 0.0f;
-#pragma unroll
-                        for (int z = 0; z < 8; ++z) {
-                            float lo, hi;
-                            unpack2<T>(ew[z], lo, hi);
-                            x[2 * z] = __fmul_rn(lo, sc[2 * z]);
-                            x[2 * z + 1] = __fmul_rn(hi, sc[2 * z + 1]);
-                            top = fmaxf(top, fmaxf(fabsf(x[2 * z]), fabsf(x[2 * z + 1])));
-                        }
-#pragma unroll
-                        for (int d = 1; d < LPR; d <<= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
-                        // the power of two below the row's largest; 127 (times one) where there is none
-                        uint32_t ex = __float_as_uint(top) >> 23;
-                        if (ex == 0 || ex >= 254) ex = 127;
-                        const float down = __uint_as_float((254u - ex) << 23);
-                        if (live) {
-                            const int r = r_at + lr;
-                            if (sub == 0) q_exp[((used & 1u) * 2 + i) * 128 + r] = (uint8_t)ex;
-                            uint32_t hi[8], lo[8];
-#pragma unroll
-                            for (int z = 0; z < 8; ++z) {
-                                const float a0 = __fmul_rn(x[2 * z], down), a1 = __fmul_rn(x[2 * z + 1], down);
-                                hi[z] = pack2<ATT_F16>(a0, a1);
-                                if (HILO) {
-                                    float h0, h1;
-                                    unpack2<ATT_F16>(hi[z], h0, h1);
-                                    lo[z] = pack2<ATT_F16>(__fsub_rn(a0, h0), __fsub_rn(a1, h1));
-                                }
-                            }
-                            uint8_t* row = q_s + (HILO ? 0 : i) * TILE + (sub / 4) * PANEL + r * 128;
-                            const int p0 = ((2 * (sub & 3)) ^ (r & 7)) << 4, p1 = ((2 * (sub & 3) + 1) ^ (r & 7)) << 4;
-                            *reinterpret_cast<uint4*>(row + p0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                            *reinterpret_cast<uint4*>(row + p1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
-                            if (HILO) {
-                                *reinterpret_cast<uint4*>(row + TILE + p0) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-                                *reinterpret_cast<uint4*>(row + TILE + p1) = make_uint4(lo[4], lo[5], lo[6], lo[7]);
-                            }
-                        }
-                    }
+                if (narrow) {
+                    scale_rows(i, 0, rows, b0, kh, own, true, used & 1u);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane < 4) mbar_arrive(&q_full[i]);
                 }
                 ++used;
-                fence_proxy_async_smem();
-                mbar_arrive(&q_full[i]);
             }
         }
     } else if (warp >= 8) {
@@ -784,6 +806,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             w.steps = items[slot].steps;
             w.alt = items[slot].alt;
             w.own = items[slot].own;
+            w.narrow = items[slot].narrow;
             w.b0 = items[slot].b0;
             w.nreq = items[slot].nreq;
             w.kh = items[slot].kh;
@@ -794,10 +817,22 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             if (w.steps < 0) break;
             const int first = w.alt ? i : 0, stride = w.alt ? 2 : 1;
             const int rows = (w.alt ? w.nreq : min(max(w.nreq - i * TOK, 0), TOK)) * a.G;
-            // a request's own rows stand at lanes 32 .. of tile 1
-            const int lr = w.own && i && !HILO && a.G <= 96 ? r - 32 : r;
-            const bool live = lr >= 0 && lr < rows;
+            const int lr = w.narrow ? lane : r;
+            const bool live = lr < rows;
             const bool work = __any_sync(FULL_MASK, live);
+            if (I8 && !w.narrow && first < w.steps && (!HILO || i == 0)) {
+                // Q of this piece: a quarter of the tile's rows each warp
+                if (HILO) {
+                    // tile 1 reads these rows as well: its products of the piece before are done
+                    ok = __all_sync(FULL_MASK, mbar_wait_ns(&q_empty[0], (q_n & 1u) ^ 1u, SA_WAIT_NS));
+                    if (!ok) break;
+                }
+                const int begin = (warp & 3) * 32;
+                scale_rows(i, begin, min(begin + 32, rows), w.b0 + (w.alt ? 0 : i * TOK), w.kh, w.own, false, q_n & 1u);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&q_full[i]);
+            }
             float c = c0;
             float m = -INFINITY, l = 0.0f;
             for (int s = first; s < w.steps; s += stride) {
@@ -806,13 +841,70 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 tm_fence_after();
                 if (I8 && s == first) {
                     // the row's power of two (Q of this piece is in place: S came from it)
-                    const uint32_t ex = q_exp[((q_n++ & 1u) * 2 + (HILO ? 0 : i)) * 128 + r];
+                    const uint32_t ex = q_exp[((q_n++ & 1u) * 2 + (HILO ? 0 : i)) * 128 + lr];
                     c = fmaxf(__fmul_rn(c0, __uint_as_float(ex << 23)), 1.17549435e-38f);
                 }
-                if (work) {
-                    const int see = w.keys - s * SA_KEYS;
-                    const uint32_t blk = block_no + s;
-                    const bool gaps = bad[blk % SA_BAD] == blk + 1;
+                const int see = w.keys - s * SA_KEYS;
+                const uint32_t blk = block_no + s;
+                const bool gaps = bad[blk % SA_BAD] == blk + 1;
+                // a new maximum: the reference m, the sum and O move to it; false if a wait ran out
+                auto refer = [&](float bm) {
+                    const bool grow = live && !(__fmul_rn(__fsub_rn(bm, m), c) <= SA_SLACK) && bm != -INFINITY;
+                    if (s == first) {
+                        m = bm;
+                    } else if (__any_sync(FULL_MASK, grow)) {
+                        const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(__fmul_rn(__fsub_rn(m, bm), c));
+                        if (grow) m = bm;
+                        l = __fmul_rn(l, f);
+#pragma unroll 1
+                        for (int k = 0; k < D; k += 32) {
+                            uint32_t o[32];
+                            tm_ld32(o_t + k, o);
+#pragma unroll
+                            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__fmul_rn(__uint_as_float(o[q]), f));
+                            tm_st32(o_t + k, o);
+                        }
+                    }
+                };
+                if (w.narrow) {
+                    // this warp's 32 keys
+                    const int k0 = 32 * (warp & 3);
+                    uint32_t have = see - k0 >= 32 ? 0xFFFFFFFFu : see > k0 ? (1u << (see - k0)) - 1u : 0u;
+                    if (gaps) have &= key_ok[(blk % SA_BAD) * 4 + (warp & 3)];
+                    uint32_t x[32];
+                    tm_ld32(s_t + k0, x);
+                    float mx[2] = {-INFINITY, -INFINITY};
+#pragma unroll
+                    for (int k = 0; k < 32; k += 4) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) x[k + q] = (have >> (k + q)) & 1u ? x[k + q] ^ flip : 0xFF800000u;
+                        mx[0] = max3(mx[0], __uint_as_float(x[k]), __uint_as_float(x[k + 1]));
+                        mx[1] = max3(mx[1], __uint_as_float(x[k + 2]), __uint_as_float(x[k + 3]));
+                    }
+                    refer(max3(mx[0], mx[1], mx[1]));
+                    const float ms = m == -INFINITY ? 0.0f : __fmaf_rn(m, c, -SHIFT);
+                    const uint64_t c2 = f32x2(c, c), ms2 = f32x2(-ms, -ms);
+                    uint64_t sum = 0ull;
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        float lo, hi;
+                        f32x2_split(fma2(f32x2(__uint_as_float(x[2 * k]), __uint_as_float(x[2 * k + 1])), c2, ms2), lo, hi);
+                        lo = ex2(lo);
+                        hi = ex2(hi);
+                        sum = add2(sum, f32x2(lo, hi));
+                        pk[k] = pack2<MT>(lo, hi);
+                    }
+                    float s0, s1;
+                    f32x2_split(sum, s0, s1);
+                    l = __fadd_rn(l, __fadd_rn(s0, s1));
+                    tm_st16(s_t + 16 * (warp & 3), pk);
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) pk[k] = 0u;
+#pragma unroll 1
+                    for (int z = 1; z < 4; ++z) tm_st16(s_t + 16 * ((warp + z) & 3), pk);
+                    tm_wait_st();
+                } else if (work) {
                     if (flip | (see < SA_KEYS) | gaps) {
                         // the uncommon cases are put right in TMEM, to keep the common code short:
                         // a negative scale, keys that are not there
@@ -842,22 +934,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                         }
                     }
                     const float bm = max3(max3(mx[0], mx[1], mx[2]), mx[3], mx[3]);
-                    const bool grow = !(__fmul_rn(__fsub_rn(bm, m), c) <= SA_SLACK) && bm != -INFINITY;
-                    if (s == first) {
-                        m = bm;
-                    } else if (__any_sync(FULL_MASK, grow)) {
-                        const float f = !grow ? 1.0f : m == -INFINITY ? 0.0f : ex2(__fmul_rn(__fsub_rn(m, bm), c));
-                        if (grow) m = bm;
-                        l = __fmul_rn(l, f);
-#pragma unroll 1
-                        for (int k = 0; k < D; k += 32) {
-                            uint32_t o[32];
-                            tm_ld32(o_t + k, o);
-#pragma unroll
-                            for (int q = 0; q < 32; ++q) o[q] = __float_as_uint(__fmul_rn(__uint_as_float(o[q]), f));
-                            tm_st32(o_t + k, o);
-                        }
-                    }
+                    refer(bm);
                     const float ms = m == -INFINITY ? 0.0f : __fmaf_rn(m, c, -SHIFT);
                     const uint64_t c2 = f32x2(c, c), ms2 = f32x2(-ms, -ms);
                     uint64_t sum[2] = {0ull, 0ull};
@@ -901,8 +978,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             if (!ok) break;
             tm_fence_after();
             if (work) {
-                const int tile_rows = w.own ? a.G : plan.tile_rows;
-                const int64_t row = ((int64_t)w.slot * 2 + i) * tile_rows + lr;
+                const int tile_rows = w.own ? plan.own_rows : plan.tile_rows;
+                const int64_t row = ((int64_t)w.slot * 2 + i) * tile_rows + (w.narrow ? (warp & 3) * rows : 0) + lr;
                 float* o_out = ws + (w.own ? plan.own_area : 0) + row * D;
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
@@ -984,19 +1061,20 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
     for (int e = 0; e < E; ++e) acc[e] = 0.0f;
     // the pieces of a group: steps of cost k from gs on, cut at multiples of
     // width; a lane finds one piece (CTA c, tile i), 32 at a time
-    auto pieces = [&](int64_t gs, int k, int blocks, bool alt, int group, int tile, int tile_rows, int row, int64_t area,
-                      int64_t stats) {
+    // (of four copies of `narrow` rows, where that is not 0)
+    auto pieces = [&](int64_t gs, int k, int blocks, bool alt, int narrow, int group, int tile, int tile_rows, int row,
+                      int64_t area, int64_t stats) {
         const int c0 = (int)(gs / width), c1 = (int)((gs + (int64_t)k * blocks - 1) / width);
-        const int per = alt ? 2 : 1;
+        const int copies = narrow ? 4 : 1, per = alt ? 2 * copies : 1;
         for (int base = 0; base < (c1 - c0 + 1) * per; base += 32) {
-            const int c = c0 + (base + lane) / per, i = alt ? (base + lane) & 1 : tile;
+            const int c = c0 + (base + lane) / per, z = (base + lane) % per, i = alt ? z / copies : tile;
             float2 st = make_float2(-INFINITY, 0.0f);
             int64_t at = 0;
             if (c <= c1) {
                 const int64_t s0 = max(ceil_div((int64_t)c * width - gs, k), (int64_t)0);
                 const int64_t s1 = min(ceil_div((int64_t)(c + 1) * width - gs, k), (int64_t)blocks);
                 if (s1 - s0 > (alt ? i : 0)) {
-                    at = ((int64_t)(group + c) * 2 + i) * tile_rows + row;
+                    at = ((int64_t)(group + c) * 2 + i) * tile_rows + (narrow ? z % copies * narrow : 0) + row;
                     st = reinterpret_cast<const float2*>(ws + stats)[at];
                 }
             }
@@ -1043,12 +1121,12 @@ __global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_co
         int k;
         const int64_t gs = prefix_start(a, plan, pt, kh, &k);
         const int tile = alt ? 0 : q / TOK;
-        pieces(gs, k, plan.blocks, alt, pt * a.Nkv + kh, tile, plan.tile_rows, (q - tile * TOK) * a.G + g, 0,
+        pieces(gs, k, plan.blocks, alt, alt && nreq * a.G <= 32 ? nreq * a.G : 0, pt * a.Nkv + kh, tile, plan.tile_rows, (q - tile * TOK) * a.G + g, 0,
                plan.stats_area);
     }
     if (nb > 0)
         pieces(pre_cost + ((int64_t)s_before * a.Nkv + (int64_t)kh * nb) * plan.cost_own, plan.cost_own, nb, true,
-               b * a.Nkv + kh, 0, a.G, g, plan.own_area, plan.own_stats);
+               a.G <= 32 ? a.G : 0, b * a.Nkv + kh, 0, plan.own_rows, g, plan.own_area, plan.own_stats);
     const bool any = M != -INFINITY;
     const float inv = any ? __frcp_rn(L) : 0.0f;
     const int d0 = lane * E;

@@ -171,6 +171,21 @@ def test_prompt_large_scores_and_scale():
     run_prompt(q, k, v, [200], [200], scale=0.0)
 
 
+def test_prompt_nan_scores_reach_their_row_alone():
+    """A NaN query, and a NaN key for the rows that see it."""
+    g = gen(13)
+    for dtype in (BF, F16):
+        q, k, v = rnd((300, 4, 128), dtype, g), rnd((300, 2, 128), dtype, g), rnd((300, 2, 128), dtype, g)
+        want, _, bound, _ = prompt64(q, k, v, [(0, 300, 0, 300)])
+        q[70, 1, 3] = math.nan
+        k[200, 1, 7] = math.nan
+        out = kvq.prompt_attention(q, k, v, i32([0, 300]), check=True)
+        assert bool(torch.isnan(out[70, 1].float()).all()) and bool(torch.isnan(out[200:, 2:].float()).all())
+        want[70, 1] = math.nan
+        want[200:, 2:] = math.nan
+        check_rows(out, want, bound)
+
+
 def test_prompt_bad_spans_are_reported_and_left_out():
     g = gen(9)
     q, k, v = rnd((100, 4, 64), BF, g), rnd((100, 4, 64), BF, g), rnd((100, 4, 64), BF, g)
@@ -300,6 +315,26 @@ def test_shared_head_groups(heads, dtype, cache):
 def test_shared_batches(batch, dtype, cache):
     lens = [(i * 37) % 90 for i in range(batch)]
     run_shared(paged(24, lens, 1000, 8, 2, 128, 32, dtype, cache))
+
+
+@pytest.mark.parametrize("heads", [(4, 1), (40, 1), (6, 1)])
+@pytest.mark.parametrize("batch", [3, 5, 33, 43, 67])
+@pytest.mark.parametrize("dtype,cache", KINDS)
+def test_shared_groups_of_few_rows(heads, batch, dtype, cache):
+    """Batches of up to 32 rows, and batches whose last group of requests has so few."""
+    lens = [(i * 53) % 300 - 1 for i in range(batch)]
+    run_shared(paged(35, lens, 900, *heads, 64, 16, dtype, cache))
+
+
+def test_shared_nan_reaches_its_request_alone():
+    for dtype, cache in KINDS:
+        d = paged(36, [100, 40, 300, 7], 300, 8, 2, 128, 16, dtype, cache)
+        want, _, bound, _ = want_shared(d)
+        d["q"][1, 3, 5] = math.nan
+        out = call_shared(d, check=True)
+        assert bool(torch.isnan(out[1, 3].float()).all())
+        want[1, 3] = math.nan                              # not compared
+        check_rows(out, want, bound)
 
 
 @pytest.mark.parametrize("dtype,cache", KINDS)
