@@ -111,8 +111,9 @@ int64_t shared_plan(int64_t B, int64_t Nq, int64_t Nkv, int64_t D, int64_t prefi
     p->own_area = pre * D;
     p->stats_area = (pre + own) * D;
     p->own_stats = p->stats_area + 2 * pre;
+    p->before = p->own_stats + 2 * own;
     p->hilo = hilo;
-    return (p->own_stats + 2 * own) * 4;
+    return (p->before + B + 1) * 4;
 }
 
 // A cache [pages, block, Nkv, D] in boxes of up to 128 tokens of one page and
@@ -154,9 +155,10 @@ kvq_status run_shared(const SharedArgs& a, cudaStream_t s) {
     auto kernel = tma ? shared_kernel<T, C, D, true> : shared_kernel<T, C, D, false>;
     constexpr uint32_t smem = sa_smem_bytes(D, I8);
     const int64_t ctas = persistent_grid(kernel, SA_THREADS, steps < SA_MAX_CTAS ? steps : SA_MAX_CTAS, smem);
+    const int parts = steps > 0 ? (int)ctas : 0;
     if (steps > 0 && launch(kernel, (unsigned)ctas, SA_THREADS, smem, s, mq, mq1, mk, mv, a, p) != cudaSuccess) return KVQ_ERR_CUDA;
     const int hblocks = (a.Nq + SJ_THREADS / 32 - 1) / (SJ_THREADS / 32);
-    return launched(launch(shared_join_kernel<T, C, D>, (unsigned)(a.B * hblocks), SJ_THREADS, 0, s, a, p, (int)ctas,
+    return launched(launch(shared_join_kernel<T, C, D>, (unsigned)(a.B * hblocks), SJ_THREADS, 0, s, a, p, parts,
                            hblocks));
 }
 

@@ -30,13 +30,14 @@
 //                    behind the keys;
 //   warp 12          issues tcgen05.mma;
 //   warp 13          cuts the work, and loads Q where it needs no scaling;
-//   warps 14, 15     scale Q over int8 caches, tile 0 and 1, for the next piece
-//                    while the tiles' last steps run (pieces of up to 32 rows;
-//                    the softmax warps do it for larger ones: one warp alone
-//                    took 29000 cycles for 128 rows).
+//   warp 14          scales Q over int8 caches, for the next piece while the
+//                    tiles' last steps run (pieces of up to 32 rows; the
+//                    softmax warps do it for larger ones: one warp alone took
+//                    29000 cycles for 128 rows);
+//   warp 15          keys and values by TMA.
 //
 // Pages of 8, 16, 32 .. tokens come by TMA, a box of up to 128 tokens of one
-// page (warp 13 over int8 caches, 14 over 16-bit ones).  Other page sizes come
+// page.  Other page sizes come
 // by 16-byte asynchronous copies of warps 8-11, which cost those warps 790
 // cycles for a tile of 128 int8 keys, as much again as the conversion.
 //
@@ -87,6 +88,7 @@ struct SharedPlan {
     int64_t own_area;        // floats before the own slots
     int64_t stats_area;      // floats before the (maximum, sum) pairs of the prefix slots; own_stats behind
     int64_t own_stats;
+    int64_t before;          // floats before the int32 counts of own steps ahead of each request, and of all
     int32_t hilo;
 };
 
@@ -101,8 +103,11 @@ struct SharedItem {
     int32_t slot;
 };
 
-// ceil(x / k) for x of either sign, k > 0
-__device__ __forceinline__ int64_t ceil_div(int64_t x, int64_t k) { return x > 0 ? (x + k - 1) / k : -((-x) / k); }
+// ceil(x / k) for x >= 0 and one of the costs
+__device__ __forceinline__ int64_t ceil_div(int64_t x, int k) {
+    static_assert(SA_COST2 == 3 && SA_COST1 == 2 && SA_COST_OWN8 == 2 && SA_COST_OWN16 == 3, "divisions by constants");
+    return k == 2 ? (x + 1) / 2 : (x + 2) / 3;
+}
 
 __device__ __forceinline__ int32_t own_blocks(const SharedArgs& a, int b) {
     const int32_t n = __ldg(a.seq_lens + b);
@@ -141,9 +146,18 @@ __device__ __forceinline__ void i8x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi)
     hi = *reinterpret_cast<uint32_t*>(&b);
 }
 
-// position of step s's keys and values in the order K0 K1 V0 K2 V1 ... V(n-1)
-__device__ __forceinline__ uint32_t k_pos(int s) { return s == 0 ? 0u : 2u * s - 1u; }
-__device__ __forceinline__ uint32_t v_pos(int s, int n) { return s == n - 1 ? 2u * n - 1u : 2u * s + 2u; }
+// The order in which a piece's tiles are loaded, which is that of their use:
+// K0 K1 V0 K2 V1 .. V(n-1) where the tiles of rows take the steps in turn, else
+// K0 V0 K1 V1 ..  Tile q of 2 n: whether it holds values, and its step.
+__device__ __forceinline__ bool tile_of(int q, int n, bool alt, int* step) {
+    if (!alt) {
+        *step = q >> 1;
+        return q & 1;
+    }
+    const bool is_v = q > 0 && ((q & 1) == 0 || q == 2 * n - 1);
+    *step = q == 0 ? 0 : is_v ? (q == 2 * n - 1 ? n - 1 : (q - 2) / 2) : (q + 1) / 2;
+    return is_v;
+}
 
 // TMA load of box {x, y, z, w} of a cache [pages, block, Nkv, D]
 __device__ __forceinline__ void tma_load_page(uint32_t dst, const CUtensorMap* map, int32_t x, int32_t head, int32_t token,
@@ -214,7 +228,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         }
         for (int i = 0; i < SA_ITEMS; ++i) {
             mbar_init(&item_full[i], 1);
-            mbar_init(&item_empty[i], HILO ? 14 : I8 ? 15 : TM ? 14 : 13);     // 8 softmax warps, 8-11, 12, and those of 14, 15 in use
+            mbar_init(&item_empty[i], 13 + (I8 ? 1 : 0) + (TM ? 1 : 0));       // 8 softmax warps, 8-11, 12, and those of 14, 15 in use
         }
         for (int i = 0; i < NS; ++i) {
             mbar_init(&kv_full[i], !I8 && TM ? 5 : 128);         // by TMA: the issuer and warps 8-11
@@ -252,15 +266,14 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     // The K and V tiles of a piece by TMA, all lanes of one warp: a lane for
     // each stretch of `box` tokens that lies in one page.  `tile_no` and
     // `step_no` count over all pieces.
-    auto load_tiles = [&](int n, int own, int b0, int kh, int key0, int keys, uint32_t& tile_no, uint32_t& step_no,
+    auto load_tiles = [&](int n, bool alt, int own, int b0, int kh, int key0, int keys, uint32_t& tile_no, uint32_t& step_no,
                           uint32_t& tails) -> bool {
         constexpr int EB = I8 ? 1 : 2;
         const int32_t* list = own ? a.table + (int64_t)b0 * a.table_stride : a.prefix_table;
         const int box = min(a.block, SA_KEYS), pieces = SA_KEYS / box;
         for (int q = 0; q < 2 * n; ++q, ++tile_no) {
-            // the order K0 K1 V0 K2 V1 ... V(n-1)
-            const bool is_v = q > 0 && ((q & 1) == 0 || q == 2 * n - 1);
-            const int s = q == 0 ? 0 : is_v ? (q == 2 * n - 1 ? n - 1 : (q - 2) / 2) : (q + 1) / 2;
+            int s;
+            const bool is_v = tile_of(q, n, alt, &s);
             const int t = s * SA_KEYS + lane * box;
             const bool wanted = lane < pieces && t < keys;
             int32_t page = -1;
@@ -400,79 +413,77 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
     if (warp == 13) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---------------- work, and Q where TMA can bring it ----------------
-        uint32_t n_item = 0, q_n[2] = {0, 0}, tile_no = 0, step_no = 0, tails = 0;
+        uint32_t n_item = 0, q_n[2] = {0, 0};
         const int64_t hi = min((int64_t)(blockIdx.x + 1) * width, total);
         int64_t at = (int64_t)blockIdx.x * width;
-        int cb = 0;                                          // cursor over the requests
+        // where the last piece was: a prefix group, or a request among the 32 whose steps the
+        // lanes hold (cb: the first one, not loaded yet at -32; cstart: where their steps start)
+        int pt = 0, cb = -32;
         int64_t cstart = pre_cost;
+        int32_t nb = 0, incl = 0;
         bool dead = false;
         while (!dead) {
             SharedItem w;
             w.steps = -1;
             while (at < hi && w.steps <= 0) {
                 int64_t gs;
-                int32_t blocks, len, g;
+                int32_t blocks, len;
                 int k;
                 if (at < pre_cost) {
-                    const int full = HILO ? SA_COST1 : SA_COST2;
-                    int pt = (int)(at / ((int64_t)plan.blocks * a.Nkv * full));
-                    if (pt > plan.n_groups - 1) pt = plan.n_groups - 1;
+                    int next;
+                    while (pt + 1 < plan.n_groups && prefix_start(a, plan, pt + 1, 0, &next) <= at) ++pt;
                     gs = prefix_start(a, plan, pt, 0, &k);
-                    const int kh = (int)((at - gs) / ((int64_t)k * plan.blocks));
-                    gs += (int64_t)kh * k * plan.blocks;
                     w.own = 0;
                     w.b0 = pt * plan.group;
                     w.nreq = min(plan.group, a.B - w.b0);
                     w.alt = HILO || w.nreq <= TOK;
-                    w.kh = kh;
                     blocks = plan.blocks;
                     len = a.prefix_len;
-                    g = pt * a.Nkv + kh;
+                    w.slot = pt * a.Nkv;
                 } else {
-                    // the request whose steps hold this place
-                    bool found = false;
                     k = plan.cost_own;
-                    blocks = 0;
-                    gs = 0;
-                    w.b0 = 0;
-                    while (!found && cb < a.B) {
-                        const int32_t nb = cb + lane < a.B ? own_blocks(a, cb + lane) : 0;
-                        int32_t incl = nb;
+                    unsigned past = 0;
+                    for (;;) {
+                        past = __ballot_sync(FULL_MASK, cb >= 0 && cstart + (int64_t)incl * a.Nkv * k > at);
+                        if (past) break;
+                        cstart += (int64_t)__shfl_sync(FULL_MASK, incl, 31) * a.Nkv * k;
+                        cb += 32;
+                        if (cb >= a.B) break;
+                        nb = cb + lane < a.B ? own_blocks(a, cb + lane) : 0;
+                        incl = nb;
 #pragma unroll
                         for (int d = 1; d < 32; d <<= 1) {
                             const int32_t y = __shfl_up_sync(FULL_MASK, incl, d);
                             if (lane >= d) incl += y;
                         }
-                        const unsigned past = __ballot_sync(FULL_MASK, cstart + (int64_t)incl * a.Nkv * k > at);
-                        if (past) {
-                            const int src = __ffs(past) - 1;
-                            found = true;
-                            w.b0 = cb + src;
-                            blocks = __shfl_sync(FULL_MASK, nb, src);
-                            gs = cstart + (int64_t)(__shfl_sync(FULL_MASK, incl, src) - blocks) * a.Nkv * k;
-                        } else {
-                            cstart += (int64_t)__shfl_sync(FULL_MASK, incl, 31) * a.Nkv * k;
-                            cb += 32;
-                        }
                     }
-                    if (!found) break;
-                    w.kh = (int)((at - gs) / ((int64_t)k * blocks));
-                    gs += (int64_t)w.kh * k * blocks;
+                    if (!past) break;
+                    const int src = __ffs(past) - 1;
+                    w.b0 = cb + src;
+                    blocks = __shfl_sync(FULL_MASK, nb, src);
+                    gs = cstart + (int64_t)(__shfl_sync(FULL_MASK, incl, src) - blocks) * a.Nkv * k;
                     w.own = 1;
                     w.nreq = 1;
                     w.alt = 1;
                     len = __ldg(a.seq_lens + w.b0);
-                    g = w.b0 * a.Nkv + w.kh;
+                    w.slot = w.b0 * a.Nkv;
                 }
-                const int64_t s0 = max(ceil_div((int64_t)blockIdx.x * width - gs, k), (int64_t)0);
-                const int64_t s1 = min(ceil_div(hi - gs, k), (int64_t)blocks);
-                at = gs + (int64_t)k * blocks;
+                const int64_t cost = (int64_t)k * blocks;
+                w.kh = 0;
+                while (gs + cost <= at) {
+                    gs += cost;
+                    ++w.kh;
+                }
+                // the steps that start in this CTA's part (divisions only at its ends)
+                const int32_t s0 = at > gs ? (int32_t)ceil_div(at - gs, k) : 0;
+                const int32_t s1 = gs + cost <= hi ? blocks : (int32_t)min(ceil_div(hi - gs, k), (int64_t)blocks);
+                at = gs + cost;
                 if (s1 > s0) {
-                    w.steps = (int32_t)(s1 - s0);
-                    w.key0 = (int32_t)s0 * SA_KEYS;
+                    w.steps = s1 - s0;
+                    w.key0 = s0 * SA_KEYS;
                     w.keys = min(len - w.key0, w.steps * SA_KEYS);
                     w.narrow = w.alt && w.nreq * a.G <= 32;
-                    w.slot = g + (int)blockIdx.x;
+                    w.slot += w.kh + (int)blockIdx.x;
                 }
             }
             const uint32_t slot = n_item % SA_ITEMS;
@@ -516,9 +527,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 }
             }
             dead = __shfl_sync(FULL_MASK, dead, 0);
-            if (I8 && TM) dead = !load_tiles(w.steps, w.own, w.b0, w.kh, w.key0, w.keys, tile_no, step_no, tails);
         }
-        if (I8 && TM) drain_tiles(tile_no);
         if (!I8 && lane == 0)
             for (int i = 0; i < 2; ++i)
                 if (q_n[i] > 0) mbar_wait_ns(&q_full[i], (q_n[i] - 1) & 1u, SA_WAIT_NS);
@@ -529,11 +538,19 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         {
             constexpr bool BF = MT == ATT_BF16;
             constexpr uint32_t ID_S = umma_idesc(BF, false, 128, SA_KEYS), ID_O = umma_idesc(BF, true, 128, D);
-            uint32_t pos = 0, q_n[2] = {0, 0}, p_n[2] = {0, 0};
-            auto wait_kv = [&](uint32_t k) { return all_wait(&kv_full[k % NS], (k / NS) & 1u, SA_WAIT_NS); };
-            auto scores = [&](int i, uint32_t k) {
-                const uint32_t qd = umma_desc_k(smem_u32(q_s + (HILO ? 0 : i) * TILE));
-                const uint32_t kd = umma_desc_k(smem_u32(kv_s + (k % NS) * TILE));
+            // tiles are used in the order of the ring: one stage and parity to follow
+            uint32_t st = 0, turn = 0, q_turn = 0, p_turn = 0;                            // q_turn, p_turn: a bit per tile
+            auto wait_kv = [&]() { return all_wait(&kv_full[st], turn, SA_WAIT_NS); };
+            auto next_kv = [&]() {
+                if (++st == NS) {
+                    st = 0;
+                    turn ^= 1u;
+                }
+            };
+            const uint32_t q0 = umma_desc_k(smem_u32(q_s)), k0 = umma_desc_k(smem_u32(kv_s)),
+                           v0 = umma_desc_mn(smem_u32(kv_s), PANEL);
+            auto scores = [&](int i) {
+                const uint32_t qd = q0 + (HILO ? 0 : i) * (TILE >> 4), kd = k0 + st * (TILE >> 4);
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
@@ -543,12 +560,21 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 }
                 umma_done(&s_full[i], lead);
             };
-            auto values = [&](int i, uint32_t k, bool first) {
-                const uint32_t vd = umma_desc_mn(smem_u32(kv_s + (k % NS) * TILE), PANEL);
+            auto values = [&](int i, bool first) {
+                const uint32_t vd = v0 + st * (TILE >> 4), d_at = tmem + O_COL + D * i, p_at = tmem + 128 * i;
                 tm_fence_after();
 #pragma unroll
-                for (int d = 0; d < SA_KEYS / 16; ++d)
-                    umma_ts(tmem + O_COL + D * i, tmem + 128 * i + 8 * d, vd + 128 * d, ID_O, !first || d != 0, lead);
+                for (int d = 0; d < SA_KEYS / 16; ++d) umma_ts(d_at, p_at + 8 * d, vd + 128 * d, ID_O, !first || d != 0, lead);
+            };
+            auto wait_q = [&](int i) {
+                const uint32_t parity = q_turn >> i & 1u;
+                q_turn ^= 1u << i;
+                return all_wait(&q_full[i], parity, SA_WAIT_NS);
+            };
+            auto wait_p = [&](int i) {
+                const uint32_t parity = p_turn >> i & 1u;
+                p_turn ^= 1u << i;
+                return all_wait(&p_ready[i], parity, SA_WAIT_NS);
             };
             bool ok = true;
             for (uint32_t n_item = 0; ok; ++n_item) {
@@ -560,82 +586,131 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 if (n < 0) break;
                 // the first scores of each tile
                 for (int i = 0; i < 2 && ok; ++i) {
-                    const int s = alt ? i : 0;
-                    if (s >= n) break;
-                    if (!HILO || i == 0) ok = all_wait(&q_full[i], q_n[i]++ & 1u, SA_WAIT_NS);
-                    ok = ok && wait_kv(pos + k_pos(s));
+                    if (alt && i >= n) break;
+                    if (!HILO || i == 0) ok = wait_q(i);
+                    ok = ok && (i == 1 && !alt ? true : wait_kv());
                     if (!ok) break;
-                    scores(i, pos + k_pos(s));
-                    if (alt) umma_done(&kv_empty[(pos + k_pos(s)) % NS], lead);
-                    if (!HILO && (alt ? s + 2 >= n : n == 1)) umma_done(&q_empty[i], lead);
+                    scores(i);
+                    if (!HILO && (alt ? i + 2 >= n : n == 1)) umma_done(&q_empty[i], lead);
+                    if (alt || i == 1) {
+                        umma_done(&kv_empty[st], lead);
+                        next_kv();
+                    }
                 }
-                if (ok && !alt) umma_done(&kv_empty[pos % NS], lead);
-                for (int s = 0; s < n && ok; ++s) {
-                    const uint32_t v = pos + v_pos(s, n);
-                    ok = wait_kv(v);
-                    for (int i = alt ? s & 1 : 0; i < (alt ? (s & 1) + 1 : 2) && ok; ++i) {
-                        ok = all_wait(&p_ready[i], p_n[i]++ & 1u, SA_WAIT_NS);
+                if (alt) {
+                    for (int s = 0; s < n && ok; ++s) {
+                        const int i = s & 1;
+                        ok = wait_kv() && wait_p(i);
                         if (!ok) break;
-                        values(i, v, s < (alt ? 2 : 1));
-                        const int nx = s + (alt ? 2 : 1);
-                        if (nx >= n) {
+                        values(i, s < 2);
+                        umma_done(&kv_empty[st], lead);
+                        next_kv();
+                        if (s + 2 >= n) {
                             umma_done(&o_full[i], lead);
                         } else {
-                            const uint32_t k = pos + k_pos(nx);
-                            ok = wait_kv(k);
+                            ok = wait_kv();
                             if (!ok) break;
-                            scores(i, k);
-                            if (alt || i == 1) umma_done(&kv_empty[k % NS], lead);
-                            if (!HILO && nx + (alt ? 2 : 1) >= n) umma_done(&q_empty[i], lead);
+                            scores(i);
+                            umma_done(&kv_empty[st], lead);
+                            next_kv();
+                            if (!HILO && s + 4 >= n) umma_done(&q_empty[i], lead);
                         }
                     }
-                    if (ok) umma_done(&kv_empty[v % NS], lead);
+                } else {
+                    for (int s = 0; s < n && ok; ++s) {
+                        const uint32_t vs = st, vt = turn;
+                        ok = wait_kv();
+                        next_kv();
+                        const bool more = s + 1 < n;
+                        const uint32_t ks = st, kt = turn;
+                        for (int i = 0; i < 2 && ok; ++i) {
+                            ok = wait_p(i);
+                            if (!ok) break;
+                            st = vs;
+                            turn = vt;
+                            values(i, s == 0);
+                            st = ks;
+                            turn = kt;
+                            if (!more) {
+                                umma_done(&o_full[i], lead);
+                            } else {
+                                ok = wait_kv();
+                                if (!ok) break;
+                                scores(i);
+                                if (s + 2 == n) umma_done(&q_empty[i], lead);
+                            }
+                        }
+                        if (!ok) break;
+                        umma_done(&kv_empty[vs], lead);
+                        if (more) {
+                            umma_done(&kv_empty[ks], lead);
+                            next_kv();
+                        }
+                    }
                 }
                 if (HILO && ok) umma_done(&q_empty[0], lead);
-                pos += 2 * n;
             }
             umma_done(drain, lead);
             all_wait(drain, 0u, SA_WAIT_NS);
         }
     } else if (warp >= 14) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
-        if (!I8 && TM && warp == 14) {
-            // ---------------- K and V tiles, 16-bit ----------------
+        if (TM && warp == 15) {
+            // ---------------- K and V tiles ----------------
             uint32_t tile_no = 0, step_no = 0, tails = 0;
             for (uint32_t n_item = 0;; ++n_item) {
                 const uint32_t slot = n_item % SA_ITEMS;
                 if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
                 const int n = items[slot].steps, own = items[slot].own, b0 = items[slot].b0, kh = items[slot].kh;
+            const bool alt = items[slot].alt != 0;
                 const int key0 = items[slot].key0, keys = items[slot].keys;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&item_empty[slot]);
-                if (n < 0 || !load_tiles(n, own, b0, kh, key0, keys, tile_no, step_no, tails)) break;
+                if (n < 0 || !load_tiles(n, alt, own, b0, kh, key0, keys, tile_no, step_no, tails)) break;
             }
             drain_tiles(tile_no);
         }
         // ---------------- Q times the key scale ----------------
-        if (I8 && !(HILO && warp == 15)) {
-            const int i = warp - 14;
-            uint32_t used = 0;
-            for (uint32_t n_item = 0;; ++n_item) {
+        if (blockIdx.x == 0 && warp == 14) {
+            // for the join: the own steps of the requests before each one
+            int32_t* before = reinterpret_cast<int32_t*>(reinterpret_cast<float*>(a.workspace) + plan.before);
+            int32_t sum = 0;
+            for (int b0 = 0; b0 < a.B; b0 += 32) {
+                const int32_t nb = b0 + lane < a.B ? own_blocks(a, b0 + lane) : 0;
+                int32_t incl = nb;
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const int32_t y = __shfl_up_sync(FULL_MASK, incl, d);
+                    if (lane >= d) incl += y;
+                }
+                if (b0 + lane < a.B) before[b0 + lane] = sum + incl - nb;
+                sum += __shfl_sync(FULL_MASK, incl, 31);
+            }
+            if (lane == 0) before[a.B] = sum;
+        }
+        if (I8 && warp == 14) {
+            uint32_t used[2] = {0, 0};
+            bool ok = true;
+            for (uint32_t n_item = 0; ok; ++n_item) {
                 const uint32_t slot = n_item % SA_ITEMS;
                 if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
                 const int steps = items[slot].steps, alt = items[slot].alt, own = items[slot].own;
                 const int nreq = items[slot].nreq, kh = items[slot].kh, narrow = items[slot].narrow;
-                const int b0 = items[slot].b0 + (alt ? 0 : i * TOK);
+                const int b0 = items[slot].b0;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&item_empty[slot]);
                 if (steps < 0) break;
-                if (i && alt && steps == 1) continue;
-                if (!__all_sync(FULL_MASK, mbar_wait_ns(&q_empty[i], (used & 1u) ^ 1u, SA_WAIT_NS))) break;
-                const int rows = (alt ? nreq : min(nreq - i * TOK, TOK)) * a.G;
-                if (narrow) {
-                    scale_rows(i, 0, rows, b0, kh, own, true, used & 1u);
-                    fence_proxy_async_smem();
-                    __syncwarp();
-                    if (lane < 4) mbar_arrive(&q_full[i]);
+                for (int i = 0; i < (HILO || (alt && steps == 1) ? 1 : 2); ++i) {
+                    ok = __all_sync(FULL_MASK, mbar_wait_ns(&q_empty[i], (used[i] & 1u) ^ 1u, SA_WAIT_NS));
+                    if (!ok) break;
+                    if (narrow) {
+                        scale_rows(i, 0, nreq * a.G, b0, kh, own, true, used[i] & 1u);
+                        fence_proxy_async_smem();
+                        __syncwarp();
+                        if (lane < 4) mbar_arrive(&q_full[i]);
+                    }
+                    ++used[i];
                 }
-                ++used;
             }
         }
     } else if (warp >= 8) {
@@ -691,6 +766,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             const uint32_t slot = n_item % SA_ITEMS;
             if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
             const int n = items[slot].steps, own = items[slot].own, b0 = items[slot].b0, kh = items[slot].kh;
+            const bool alt = items[slot].alt != 0;
             const int key0 = items[slot].key0, keys = items[slot].keys;
             __syncwarp();
             if (lane == 0) mbar_arrive(&item_empty[slot]);
@@ -740,9 +816,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             const uint32_t block0 = block_no;
             uint32_t next = lookup(0);
             for (int q = 0; q < 2 * n && ok; ++q) {
-                // the order K0 K1 V0 K2 V1 ... V(n-1)
-                const bool is_v = q > 0 && ((q & 1) == 0 || q == 2 * n - 1);
-                const int s = q == 0 ? 0 : is_v ? (q == 2 * n - 1 ? n - 1 : (q - 2) / 2) : (q + 1) / 2;
+                int s;
+                const bool is_v = tile_of(q, n, alt, &s);
                 if (!I8) {
                     ok = __all_sync(FULL_MASK, mbar_wait_ns(&kv_empty[issued % NS], ((issued / NS) & 1u) ^ 1u, SA_WAIT_NS));
                     if (!ok) break;
@@ -1016,117 +1091,156 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
 constexpr int SJ_THREADS = 256;
 
 template <int T, int C, int D>
-__global__ void __launch_bounds__(SJ_THREADS) shared_join_kernel(const __grid_constant__ SharedArgs a,
+__global__ void __launch_bounds__(SJ_THREADS, 4) shared_join_kernel(const __grid_constant__ SharedArgs a,
                                                                 const __grid_constant__ SharedPlan plan, int ctas,
                                                                 int hblocks) {
     constexpr bool HILO = C == ATT_I8 && T == ATT_F16;
     constexpr int E = D / 32;
-    __shared__ int s_all, s_before;
     __shared__ int64_t s_at[SJ_THREADS / 32][32];            // the pieces found: where and how much
     __shared__ float s_w[SJ_THREADS / 32][32];
-    const int lane = threadIdx.x & 31;
-    if (threadIdx.x == 0) s_all = s_before = 0;
-    __syncthreads();
-    pdl_wait();
-    pdl_trigger();
-    const int b = blockIdx.x / hblocks;
-    {
-        int n = 0, before = 0;
-        for (int k = threadIdx.x; k < a.B; k += SJ_THREADS) {
-            const int nb = own_blocks(a, k);
-            n += nb;
-            before += k < b ? nb : 0;
-        }
-        n = __reduce_add_sync(FULL_MASK, n);
-        before = __reduce_add_sync(FULL_MASK, before);
-        if (lane == 0) {
-            atomicAdd(&s_all, n);
-            atomicAdd(&s_before, before);
-        }
-    }
-    __syncthreads();
-    const int64_t pre_cost = prefix_cost(a, plan);
-    const int64_t total = pre_cost + (int64_t)s_all * a.Nkv * plan.cost_own;
-    const int64_t width = (total + ctas - 1) / ctas;
-    if (own_length(a, b) < 0) return;
-    const int nb = own_blocks(a, b);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int b = blockIdx.x / hblocks, h = (int)(blockIdx.x % hblocks) * (SJ_THREADS / 32) + warp;
     const int TOK = 128 / a.G;
     const float* ws = reinterpret_cast<const float*>(a.workspace);
-    const int h = (int)(blockIdx.x % hblocks) * (SJ_THREADS / 32) + (threadIdx.x >> 5);
-    if (h >= a.Nq) return;
+    const int32_t* counts = reinterpret_cast<const int32_t*>(ws + plan.before);
+    pdl_wait();
+    pdl_trigger();
+    if (h >= a.Nq || own_length(a, b) < 0) return;
+    const int nb = own_blocks(a, b);
+    const int64_t pre_cost = prefix_cost(a, plan);
+    int64_t own_before = 0, own_all = 0;
+    if (ctas > 0) {
+        own_before = counts[b];
+        own_all = counts[a.B];
+    }
+    const int64_t total = pre_cost + own_all * a.Nkv * plan.cost_own;
+    const bool small = total < 0x7fffffff;                    // 32-bit divisions take a fraction of the time
+    const int64_t width = ctas == 0 ? 1 : small ? (uint32_t)(total + ctas - 1) / (uint32_t)ctas : (total + ctas - 1) / ctas;
+    auto cta_of = [&](int64_t x) { return (int)(small ? (uint32_t)x / (uint32_t)width : x / width); };
     const int kh = h / a.G, g = h - kh * a.G;
-    const int warp = threadIdx.x >> 5;
-    float M = -INFINITY, L = 0.0f, acc[E];
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
-    // the pieces of a group: steps of cost k from gs on, cut at multiples of
-    // width; a lane finds one piece (CTA c, tile i), 32 at a time
-    // (of four copies of `narrow` rows, where that is not 0)
-    auto pieces = [&](int64_t gs, int k, int blocks, bool alt, int narrow, int group, int tile, int tile_rows, int row,
-                      int64_t area, int64_t stats) {
-        const int c0 = (int)(gs / width), c1 = (int)((gs + (int64_t)k * blocks - 1) / width);
-        const int copies = narrow ? 4 : 1, per = alt ? 2 * copies : 1;
-        for (int base = 0; base < (c1 - c0 + 1) * per; base += 32) {
-            const int c = c0 + (base + lane) / per, z = (base + lane) % per, i = alt ? z / copies : tile;
-            float2 st = make_float2(-INFINITY, 0.0f);
-            int64_t at = 0;
-            if (c <= c1) {
-                const int64_t s0 = max(ceil_div((int64_t)c * width - gs, k), (int64_t)0);
-                const int64_t s1 = min(ceil_div((int64_t)(c + 1) * width - gs, k), (int64_t)blocks);
-                if (s1 - s0 > (alt ? i : 0)) {
-                    at = ((int64_t)(group + c) * 2 + i) * tile_rows + (narrow ? z % copies * narrow : 0) + row;
-                    st = reinterpret_cast<const float2*>(ws + stats)[at];
-                }
-            }
-            float top = st.x;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
-            const float mn = fmaxf(M, top);
-            if (mn == -INFINITY) continue;                    // nothing visible so far
-            const float f = exp2f(__fsub_rn(M, mn));
-            const bool has = st.x != -INFINITY;
-            const float w = has ? exp2f(__fsub_rn(st.x, mn)) : 0.0f;
-            float sum = has ? __fmul_rn(st.y, w) : 0.0f;
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(FULL_MASK, sum, d));
-            L = __fmaf_rn(L, f, sum);
-            M = mn;
-#pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = __fmul_rn(acc[e], f);
-            const unsigned mask = __ballot_sync(FULL_MASK, has);
-            const int count = __popc(mask);
-            __syncwarp();
-            if (has) {
-                const int n = __popc(mask & ((1u << lane) - 1u));
-                s_at[warp][n] = area + at * D;
-                s_w[warp][n] = w;
-            }
-            __syncwarp();
-#pragma unroll 4
-            for (int n = 0; n < count; ++n) {
-                const float* o = ws + s_at[warp][n] + lane * E;
-                const float wn = s_w[warp][n];
-                float v[E];
-                if (E == 4) *reinterpret_cast<float4*>(v) = *reinterpret_cast<const float4*>(o);
-                else *reinterpret_cast<float2*>(v) = *reinterpret_cast<const float2*>(o);
-#pragma unroll
-                for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(v[e], wn, acc[e]);
-            }
-        }
+
+    // The pieces of the row: those of its prefix group, then those of its own
+    // keys.  A group's steps of cost k start at gs and are cut at multiples of
+    // width; it has a piece for each CTA from c0 on, tile (both, where they take
+    // the steps in turn) and copy.
+    struct Group {
+        int64_t gs, base, stats;                              // base: floats before the slots
+        int32_t k, blocks, first, count, per, copies, narrow, tile, slot, tile_rows, row;
     };
-    if (plan.blocks > 0) {
+    auto group_of = [&](int64_t gs, int k, int blocks, bool alt, int narrow, int slot, int tile, int tile_rows, int row,
+                        int64_t base, int64_t stats) {
+        Group x;
+        x.gs = gs;
+        x.k = k;
+        x.blocks = blocks;
+        x.copies = narrow ? 4 : 1;
+        x.per = alt ? 2 * x.copies : 1;
+        x.first = blocks > 0 ? cta_of(gs) : 0;
+        x.count = blocks > 0 ? (cta_of(gs + (int64_t)k * blocks - 1) - x.first + 1) * x.per : 0;
+        x.narrow = narrow;
+        x.tile = alt ? -1 : tile;
+        x.slot = slot;
+        x.tile_rows = tile_rows;
+        x.row = row;
+        x.base = base;
+        x.stats = stats;
+        return x;
+    };
+    Group pre, mine;
+    {
         const int pt = b / plan.group, q = b - pt * plan.group;
         const int nreq = min(plan.group, a.B - pt * plan.group);
         const bool alt = HILO || nreq <= TOK;
-        int k;
-        const int64_t gs = prefix_start(a, plan, pt, kh, &k);
+        int k = 2;
+        int64_t gs = 0;
+        if (plan.blocks > 0) gs = prefix_start(a, plan, pt, kh, &k);
         const int tile = alt ? 0 : q / TOK;
-        pieces(gs, k, plan.blocks, alt, alt && nreq * a.G <= 32 ? nreq * a.G : 0, pt * a.Nkv + kh, tile, plan.tile_rows, (q - tile * TOK) * a.G + g, 0,
-               plan.stats_area);
+        pre = group_of(gs, k, plan.blocks, alt, alt && nreq * a.G <= 32 ? nreq * a.G : 0, pt * a.Nkv + kh, tile,
+                         plan.tile_rows, (q - tile * TOK) * a.G + g, 0, plan.stats_area);
+        mine = group_of(pre_cost + (own_before * a.Nkv + (int64_t)kh * nb) * plan.cost_own, plan.cost_own, nb, true,
+                         a.G <= 32 ? a.G : 0, b * a.Nkv + kh, 0, plan.own_rows, g, plan.own_area, plan.own_stats);
     }
-    if (nb > 0)
-        pieces(pre_cost + ((int64_t)s_before * a.Nkv + (int64_t)kh * nb) * plan.cost_own, plan.cost_own, nb, true,
-               a.G <= 32 ? a.G : 0, b * a.Nkv + kh, 0, plan.own_rows, g, plan.own_area, plan.own_stats);
+    float M = -INFINITY, L = 0.0f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.0f;
+    for (int n0 = 0; n0 < pre.count + mine.count; n0 += 32) {
+        // a lane looks at one piece
+        int n = n0 + lane;
+        const bool own = n >= pre.count;
+        if (own) n -= pre.count;
+        Group x;                                              // chosen field by field: no array in local memory
+        x.gs = own ? mine.gs : pre.gs;
+        x.base = own ? mine.base : pre.base;
+        x.stats = own ? mine.stats : pre.stats;
+        x.k = own ? mine.k : pre.k;
+        x.blocks = own ? mine.blocks : pre.blocks;
+        x.first = own ? mine.first : pre.first;
+        x.count = own ? mine.count : pre.count;
+        x.per = own ? mine.per : pre.per;
+        x.copies = own ? mine.copies : pre.copies;
+        x.narrow = own ? mine.narrow : pre.narrow;
+        x.tile = own ? mine.tile : pre.tile;
+        x.slot = own ? mine.slot : pre.slot;
+        x.tile_rows = own ? mine.tile_rows : pre.tile_rows;
+        x.row = own ? mine.row : pre.row;
+        float2 st = make_float2(-INFINITY, 0.0f);
+        int64_t at = 0;
+        if (n < x.count) {
+            const int c = x.first + n / x.per, z = n % x.per, i = x.tile < 0 ? z / x.copies : x.tile;
+            const int64_t lo = (int64_t)c * width - x.gs, hi = lo + width;
+            const int64_t s0 = lo > 0 ? ceil_div(lo, x.k) : 0;
+            const int64_t s1 = min(ceil_div(hi, x.k), (int64_t)x.blocks);
+            if (s1 - s0 > (x.tile < 0 ? i : 0)) {
+                const int64_t r = ((int64_t)(x.slot + c) * 2 + i) * x.tile_rows + z % x.copies * x.narrow + x.row;
+                st = reinterpret_cast<const float2*>(ws + x.stats)[r];
+                at = x.base + r * D;
+            }
+        }
+        float top = st.x;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) top = fmaxf(top, __shfl_xor_sync(FULL_MASK, top, d));
+        const float mn = fmaxf(M, top);
+        if (mn == -INFINITY) continue;                        // nothing visible so far
+        const float f = exp2f(__fsub_rn(M, mn));
+        const bool has = st.x != -INFINITY;
+        const float w = has ? exp2f(__fsub_rn(st.x, mn)) : 0.0f;
+        float sum = has ? __fmul_rn(st.y, w) : 0.0f;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum = __fadd_rn(sum, __shfl_xor_sync(FULL_MASK, sum, d));
+        L = __fmaf_rn(L, f, sum);
+        M = mn;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] = __fmul_rn(acc[e], f);
+        const unsigned mask = __ballot_sync(FULL_MASK, has);
+        const int count = __popc(mask);
+        __syncwarp();
+        if (has) {
+            const int to = __popc(mask & ((1u << lane) - 1u));
+            s_at[warp][to] = at;
+            s_w[warp][to] = w;
+        }
+        __syncwarp();
+        // 4 rows in flight: one after the other they cost a memory latency each
+        for (int r0 = 0; r0 < count; r0 += 4) {
+            float v[4][E];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (r0 + r < count) {
+                    const float* o = ws + s_at[warp][r0 + r] + lane * E;
+                    if (E == 4) *reinterpret_cast<float4*>(v[r]) = *reinterpret_cast<const float4*>(o);
+                    else *reinterpret_cast<float2*>(v[r]) = *reinterpret_cast<const float2*>(o);
+                }
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                if (r0 + r < count) {
+                    const float wr = s_w[warp][r0 + r];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] = __fmaf_rn(v[r][e], wr, acc[e]);
+                }
+            }
+        }
+    }
     const bool any = M != -INFINITY;
     const float inv = any ? __frcp_rn(L) : 0.0f;
     const int d0 = lane * E;
