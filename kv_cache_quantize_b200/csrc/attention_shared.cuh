@@ -24,6 +24,10 @@
 // each copy takes 32 of the step's keys, its weights of the others being zero.
 // The four are pieces of their own for the join.
 //
+// Q has two buffers.  A piece of two tiles of rows fills both; others use them
+// in turn, one for both tiles, so that the next piece's Q is in place before
+// its turn (f16 queries over int8 pages take both, for two values each).
+//
 //   warps 0-3, 4-7   softmax of tile 0 and 1, a thread per row;
 //   warps 8-11       int8 codes to f16 (exactly), from raw tiles into the
 //                    product's; over 16-bit caches, zeros in V's last rows
@@ -332,7 +336,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             mbar_wait_ns(I8 ? &raw_full[k % R] : &kv_full[k % R], (k / R) & 1u, SA_WAIT_NS);
     };
 
-    // Rows [begin, end) of tile i's Q (requests from b0 on) times the key scale,
+    // Rows [begin, end) of Q (requests from b0 on) times the key scale into buffer i,
     // by one warp: LPR lanes share a row, 16 channels each.
     auto scale_rows = [&](int i, int begin, int end, int b0, int kh, int own, bool copies, uint32_t parity) {
         constexpr int LPR = D / 16, RPP = 32 / LPR;          // rows of a pass
@@ -395,7 +399,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                         }
                     }
                     for (int r = lr; r < (copies ? 128 : lr + 1); r += 32) {
-                        uint8_t* row = q_s + (HILO ? 0 : i) * TILE + (sub / 4) * PANEL + r * 128;
+                        uint8_t* row = q_s + i * TILE + (sub / 4) * PANEL + r * 128;
                         const int p0 = ((2 * (sub & 3)) ^ (r & 7)) << 4, p1 = ((2 * (sub & 3) + 1) ^ (r & 7)) << 4;
                         *reinterpret_cast<uint4*>(row + p0) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
                         *reinterpret_cast<uint4*>(row + p1) = make_uint4(hi[4], hi[5], hi[6], hi[7]);
@@ -414,6 +418,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         // ---------------- work, and Q where TMA can bring it ----------------
         uint32_t n_item = 0, q_n[2] = {0, 0};
+        int q_next = 0;                                      // buffer of Q of the next piece that uses one
         const int64_t hi = min((int64_t)(blockIdx.x + 1) * width, total);
         int64_t at = (int64_t)blockIdx.x * width;
         // where the last piece was: a prefix group, or a request among the 32 whose steps the
@@ -506,8 +511,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             ++n_item;
             if (w.steps < 0) break;
             if (!I8 && lane == 0) {
-                for (int i = 0; i < 2 && !dead; ++i) {
-                    if (i == 1 && w.alt && w.steps == 1) continue;
+                for (int i = w.alt ? q_next : 0; i < (w.alt ? q_next + 1 : 2) && !dead; ++i) {
                     if (!mbar_wait_ns(&q_empty[i], (q_n[i] & 1u) ^ 1u, SA_WAIT_NS)) {
                         dead = true;
                         break;
@@ -526,6 +530,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                     }
                 }
             }
+            if (w.alt) q_next ^= 1;
             dead = __shfl_sync(FULL_MASK, dead, 0);
         }
         if (!I8 && lane == 0)
@@ -549,8 +554,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             };
             const uint32_t q0 = umma_desc_k(smem_u32(q_s)), k0 = umma_desc_k(smem_u32(kv_s)),
                            v0 = umma_desc_mn(smem_u32(kv_s), PANEL);
-            auto scores = [&](int i) {
-                const uint32_t qd = q0 + (HILO ? 0 : i) * (TILE >> 4), kd = k0 + st * (TILE >> 4);
+            auto scores = [&](int i, int buffer) {
+                const uint32_t qd = q0 + buffer * (TILE >> 4), kd = k0 + st * (TILE >> 4);
                 tm_fence_after();
 #pragma unroll
                 for (int d = 0; d < D / 16; ++d) {
@@ -577,6 +582,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 return all_wait(&p_ready[i], parity, SA_WAIT_NS);
             };
             bool ok = true;
+            int q_next = 0;
             for (uint32_t n_item = 0; ok; ++n_item) {
                 const uint32_t slot = n_item % SA_ITEMS;
                 if (!all_wait(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS)) break;
@@ -585,18 +591,20 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 if (lead) mbar_arrive(&item_empty[slot]);
                 if (n < 0) break;
                 // the first scores of each tile
+                const int buffer = q_next;
                 for (int i = 0; i < 2 && ok; ++i) {
                     if (alt && i >= n) break;
-                    if (!HILO || i == 0) ok = wait_q(i);
+                    if (!alt || i == 0) ok = wait_q(alt ? buffer : i);
                     ok = ok && (i == 1 && !alt ? true : wait_kv());
                     if (!ok) break;
-                    scores(i);
-                    if (!HILO && (alt ? i + 2 >= n : n == 1)) umma_done(&q_empty[i], lead);
+                    scores(i, alt ? buffer : i);
+                    if (alt ? i + 1 == n : n == 1) umma_done(&q_empty[alt ? buffer : i], lead);
                     if (alt || i == 1) {
                         umma_done(&kv_empty[st], lead);
                         next_kv();
                     }
                 }
+                if (alt && !HILO) q_next ^= 1;
                 if (alt) {
                     for (int s = 0; s < n && ok; ++s) {
                         const int i = s & 1;
@@ -610,10 +618,10 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                         } else {
                             ok = wait_kv();
                             if (!ok) break;
-                            scores(i);
+                            scores(i, buffer);
                             umma_done(&kv_empty[st], lead);
                             next_kv();
-                            if (!HILO && s + 4 >= n) umma_done(&q_empty[i], lead);
+                            if (s + 3 == n) umma_done(&q_empty[buffer], lead);
                         }
                     }
                 } else {
@@ -636,7 +644,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                             } else {
                                 ok = wait_kv();
                                 if (!ok) break;
-                                scores(i);
+                                scores(i, i);
                                 if (s + 2 == n) umma_done(&q_empty[i], lead);
                             }
                         }
@@ -648,7 +656,6 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                         }
                     }
                 }
-                if (HILO && ok) umma_done(&q_empty[0], lead);
             }
             umma_done(drain, lead);
             all_wait(drain, 0u, SA_WAIT_NS);
@@ -690,6 +697,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         }
         if (I8 && warp == 14) {
             uint32_t used[2] = {0, 0};
+            int q_next = 0;
             bool ok = true;
             for (uint32_t n_item = 0; ok; ++n_item) {
                 const uint32_t slot = n_item % SA_ITEMS;
@@ -700,7 +708,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&item_empty[slot]);
                 if (steps < 0) break;
-                for (int i = 0; i < (HILO || (alt && steps == 1) ? 1 : 2); ++i) {
+                for (int i = alt ? q_next : 0; i < (alt ? q_next + 1 : 2); ++i) {
                     ok = __all_sync(FULL_MASK, mbar_wait_ns(&q_empty[i], (used[i] & 1u) ^ 1u, SA_WAIT_NS));
                     if (!ok) break;
                     if (narrow) {
@@ -711,6 +719,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                     }
                     ++used[i];
                 }
+                if (alt && !HILO) q_next ^= 1;
             }
         }
     } else if (warp >= 8) {
@@ -872,7 +881,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         const uint32_t flip = a.scale < 0.0f ? 0x80000000u : 0u;
         constexpr float SHIFT = MT == ATT_F16 ? ATT_F16_SHIFT : 0.0f;
         float* ws = reinterpret_cast<float*>(a.workspace);
-        uint32_t s_n = 0, o_n = 0, q_n = 0, block_no = 0;
+        uint32_t s_n = 0, o_n = 0, q_n[2] = {0, 0}, block_no = 0;        // q_n: uses of the buffers of Q
+        int q_next = 0;
         bool ok = true;
         for (uint32_t n_item = 0; ok; ++n_item) {
             const uint32_t slot = n_item % SA_ITEMS;
@@ -895,18 +905,21 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             const int lr = w.narrow ? lane : r;
             const bool live = lr < rows;
             const bool work = __any_sync(FULL_MASK, live);
-            if (I8 && !w.narrow && first < w.steps && (!HILO || i == 0)) {
-                // Q of this piece: a quarter of the tile's rows each warp
-                if (HILO) {
-                    // tile 1 reads these rows as well: its products of the piece before are done
-                    ok = __all_sync(FULL_MASK, mbar_wait_ns(&q_empty[0], (q_n & 1u) ^ 1u, SA_WAIT_NS));
-                    if (!ok) break;
-                }
+            const int buffer = w.alt ? q_next : i;
+            const uint32_t use = buffer ? q_n[1] : q_n[0];
+            if (!w.alt || buffer == 0) ++q_n[0];
+            if (!w.alt || buffer == 1) ++q_n[1];
+            if (w.alt && !HILO) q_next ^= 1;
+            if (I8 && !w.narrow && (!w.alt || i == 0)) {
+                // Q of this piece: a quarter of the rows each warp, once the products that read the
+                // buffer before are done
+                ok = __all_sync(FULL_MASK, mbar_wait_ns(&q_empty[buffer], (use & 1u) ^ 1u, SA_WAIT_NS));
+                if (!ok) break;
                 const int begin = (warp & 3) * 32;
-                scale_rows(i, begin, min(begin + 32, rows), w.b0 + (w.alt ? 0 : i * TOK), w.kh, w.own, false, q_n & 1u);
+                scale_rows(buffer, begin, min(begin + 32, rows), w.b0 + (w.alt ? 0 : i * TOK), w.kh, w.own, false, use & 1u);
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&q_full[i]);
+                if (lane == 0) mbar_arrive(&q_full[buffer]);
             }
             float c = c0;
             float m = -INFINITY, l = 0.0f;
@@ -916,7 +929,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 tm_fence_after();
                 if (I8 && s == first) {
                     // the row's power of two (Q of this piece is in place: S came from it)
-                    const uint32_t ex = q_exp[((q_n++ & 1u) * 2 + (HILO ? 0 : i)) * 128 + lr];
+                    const uint32_t ex = q_exp[((use & 1u) * 2 + buffer) * 128 + lr];
                     c = fmaxf(__fmul_rn(c0, __uint_as_float(ex << 23)), 1.17549435e-38f);
                 }
                 const int see = w.keys - s * SA_KEYS;
@@ -1045,10 +1058,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             }
             if (!ok) break;
             block_no += w.steps;
-            if (first >= w.steps) {
-                if (HILO) ++q_n;                              // the exponents count tile 0's pieces
-                continue;
-            }
+            if (first >= w.steps) continue;
             ok = __all_sync(FULL_MASK, mbar_wait_ns(&o_full[i], o_n++ & 1u, SA_WAIT_NS));
             if (!ok) break;
             tm_fence_after();
