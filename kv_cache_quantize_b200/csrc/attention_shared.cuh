@@ -79,7 +79,7 @@ __host__ __device__ constexpr uint32_t sa_smem_bytes(int D, bool i8) {
 
 // the cost of a step: two tiles of rows, one tile (prefix), a request's own
 // keys (int8, 16-bit)
-constexpr int SA_COST2 = 3, SA_COST1 = 2, SA_COST_OWN8 = 2, SA_COST_OWN16 = 3;
+constexpr int SA_COST2 = 3, SA_COST1 = 2, SA_COST_OWN8 = 2, SA_COST_OWN16 = 2;
 
 struct SharedPlan {
     int32_t group;           // requests of a prefix group
@@ -109,7 +109,7 @@ struct SharedItem {
 
 // ceil(x / k) for x >= 0 and one of the costs
 __device__ __forceinline__ int64_t ceil_div(int64_t x, int k) {
-    static_assert(SA_COST2 == 3 && SA_COST1 == 2 && SA_COST_OWN8 == 2 && SA_COST_OWN16 == 3, "divisions by constants");
+    static_assert(SA_COST2 == 3 && SA_COST1 == 2 && SA_COST_OWN8 == 2 && SA_COST_OWN16 == 2, "divisions by constants");
     return k == 2 ? (x + 1) / 2 : (x + 2) / 3;
 }
 
