@@ -163,6 +163,20 @@ def test_prompt_infinite_values_that_are_seen(bad):
     assert bool(torch.isfinite(out[:, :, keep].float()).all())
 
 
+def test_prompt_offsets_beyond_32_bits():
+    """Token rows a megabyte apart: q, k, v and out in one buffer of more than 2^32 elements."""
+    t, step = 4500, 1 << 20
+    big = torch.empty((t * step,), dtype=BF, device="cuda")
+    at = [big[1024 * i:].as_strided((t, h, 64), (step, 64, 1)) for i, h in enumerate((4, 2, 2, 4))]
+    g = gen(14)
+    for x in at[:3]:
+        x.copy_(rnd(x.shape, BF, g))
+    q, k, v, out = at
+    kvq.prompt_attention(q, k, v, i32([0, 4200, t]), out=out, check=True)
+    want, _, bound, _ = prompt64(q[4200:], k[4200:], v[4200:], [(0, 300, 0, 300)])
+    check_rows(out[4200:], want, bound)
+
+
 def test_prompt_large_scores_and_scale():
     g = gen(8)
     q, k, v = rnd((200, 4, 64), BF, g, 30.0), rnd((200, 4, 64), BF, g, 30.0), rnd((200, 4, 64), BF, g)
@@ -396,6 +410,31 @@ def test_shared_strides_and_views():
     d["table"] = d["table"][:1].expand(4, -1)              # all requests on one row, stride 0
     d["lens"] = i32([40, 12, 33, 0])
     run_shared(d)
+
+
+@pytest.mark.parametrize("block", [64, 24])
+def test_shared_offsets_beyond_32_bits(block):
+    """Pages at the end of a cache of more than 4 GB."""
+    d = paged(37, [300, 10], 200, 8, 4, 128, block, BF, I8)
+    few = d["kc"].shape[0]
+    pages = (9 << 29) // (block * 4 * 128)                       # 4.5 GB
+    far = torch.zeros((pages, block, 4, 128), dtype=I8, device="cuda")
+    far[pages - few:] = d["kc"]
+    want, wl, bound, lb = want_shared({**d, "vc": d["kc"]})
+    d["table"] = torch.where(d["table"] >= 0, d["table"] + pages - few, -1).to(torch.int32)
+    d["prefix_table"] = d["prefix_table"] + pages - few
+    check_rows(call_shared({**d, "kc": far, "vc": far}, check=True), want, bound)
+
+
+def test_shared_without_pages_or_requests():
+    for dtype, cache in KINDS:
+        d = paged(38, [0, -1, 0], 0, 8, 2, 64, 16, dtype, cache)
+        out = run_shared(d)
+        assert bool((out[[0, 2]] == 0).all())
+        empty = {**d, "kc": d["kc"][:0], "vc": d["vc"][:0]}
+        assert bool((call_shared(empty, check=True)[[0, 2]] == 0).all())
+        none = {**d, "q": d["q"][:0], "table": d["table"][:0], "lens": d["lens"][:0]}
+        assert call_shared(none, check=True).shape == (0, 8, 64)
 
 
 def test_shared_bad_pages_and_lengths_are_reported_and_left_out():
