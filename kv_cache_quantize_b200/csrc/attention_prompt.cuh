@@ -9,7 +9,7 @@
 // A query tile holds 128 rows: 128 / G consecutive tokens x the G query heads
 // that read one key head, so a short prompt fills its tiles with heads and K
 // and V are read once for all of them.  One CTA per SM works on two such tiles
-// at a time (rows of TMEM: S0, S1, O0, O1 take all 512 columns at D = 128), so
+// at a time (columns of TMEM: S0, S1, O0, O1 take all 512 columns at D = 128), so
 // that the tensor core multiplies for one tile while the other one's softmax
 // runs:
 //   warps 0-3, 4-7  softmax of tile 0 and 1: a thread owns a row; S from
@@ -19,10 +19,21 @@
 //                   block j + 1, tile 0 and tile 1 in turn;
 //   warp 9          work items and TMA: the grid has a CTA for every item, but a
 //                   running CTA takes over items whose CTAs have not started
-//                   (cluster launch control), heavy ones first; Q tiles, and a ring of K and V tiles of
-//                   128 keys (128-byte swizzle).
+//                   (cluster launch control), heavy ones first (against a
+//                   fixed assignment 243 -> 215 us for 24 prompts of 1 to
+//                   2048 tokens); Q tiles, and a ring of K and V tiles of 128
+//                   keys (128-byte swizzle; 5 stages, 4 cost 4 %).
 // The tensor pipe executes a CTA's products in order, so Q K^T of block j + 1
 // may overwrite the columns that P V of block j reads.
+//
+// What bounds it: a tile's softmax (about 1980 cycles for 128 keys) and its two
+// products (1030 and their latencies) take turns, and two tiles cover each other
+// only in part: 3400 cycles for 128 keys of both, where the products alone take
+// 2160 (tensor pipe 56 % active).  One prompt of 16384 tokens, 16 / 4 heads of
+// 128, bf16: 862 us, 1278 TFLOP/s, 0.78 of the measured peak on a cold card;
+// 0.68 in a loop, where the power cap lowers the clock.  An item's start and end
+// cost about three blocks, so short prompts are slower: 24 of 1 to 2048 tokens
+// 205 us, 660 TFLOP/s.
 //
 // A row's weights are rounded to the 16-bit type of V for the product (half a
 // step, the rounding that the output itself gets); their sum is taken before.
@@ -115,6 +126,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         mbar_init(drain, 1);
         mbar_init_fence();
     }
+    if (warp == 9 && lane < 3) tma_prefetch_map(lane == 0 ? &tm_q : lane == 1 ? &tm_k : &tm_v);
     if (warp == 8) tm_alloc(tmem_slot, 512);
     tm_fence_before();
     __syncthreads();

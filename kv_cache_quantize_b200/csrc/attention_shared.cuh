@@ -40,6 +40,15 @@
 //                    29000 cycles for 128 rows);
 //   warp 15          keys and values by TMA.
 //
+// What bounds it (one B200; times of both kernels): over a long prefix the
+// chain of a tile's softmax and products, as in the prompt kernel, with the
+// scores read twice from TMEM for want of registers -- 256 requests over 32768
+// bf16 keys 87 us (0.49 of the measured peak), over int8 ones 101 us; over own
+// keys, int8, shared memory: 224 KB pass through it for a step of 128 keys (raw
+// codes in and out, f16 tiles in, operands of the products), 1750 cycles --
+// 256 requests of 512 own keys 62 us, 134 MB (2.2 TB/s); bf16 63 us, 268 MB
+// (4.3 TB/s).  One step of one request takes 10 us, two launches among it.
+//
 // Pages of 8, 16, 32 .. tokens come by TMA, a box of up to 128 tokens of one
 // page.  Other page sizes come
 // by 16-byte asynchronous copies of warps 8-11, which cost those warps 790
@@ -248,6 +257,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
         *s_blocks = 0;
         for (int i = 0; i < SA_BAD; ++i) bad[i] = 0u;
     }
+    if (TM && warp == 15 && lane < 2) tma_prefetch_map(lane ? &tm_v : &tm_k);
+    if (!I8 && warp == 13 && lane < 2) tma_prefetch_map(lane ? &tm_q1 : &tm_q);
     if (warp == 12) tm_alloc(tmem_slot, 512);
     tm_fence_before();
     __syncthreads();
@@ -1094,7 +1105,9 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
 }
 
 // ---------------------------------------------------------------------------
-// Join the pieces: one warp per request and head.  Piece i: O_i, l_i relative
+// Join the pieces: one warp per request and head, a lane finding each piece and
+// four rows in flight; 256 requests x 16 heads of 8 to 20 pieces in about 10 us
+// (latency: a chain of counts, sums and rows, each a trip to L2).  Piece i: O_i, l_i relative
 // to 2^M_i; out = sum 2^(M_i - M) O_i / sum 2^(M_i - M) l_i, then the value
 // scale and offset.
 // ---------------------------------------------------------------------------

@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(PG_THREADS) page_copy_words_kernel(const __gri
     pdl_trigger();
     page_tables<MODE>(a);
     const int64_t total = a.n_pairs * a.units;
-    if (MODE == PG_LIST) {
+    if constexpr (MODE == PG_LIST) {
         for (int64_t u = blockIdx.x; u < total; u += gridDim.x) {
             const uint8_t* src;
             uint8_t* dst;
@@ -168,43 +168,43 @@ __global__ void __launch_bounds__(PG_THREADS) page_copy_words_kernel(const __gri
             for (uint32_t k = threadIdx.x; k < n; k += PG_THREADS)
                 reinterpret_cast<W*>(dst)[k] = reinterpret_cast<const W*>(src)[k];
         }
-        return;
-    }
-    for (int64_t base = blockIdx.x; base < total; base += 32 * (int64_t)gridDim.x) {
-        const int64_t u = base + lane * (int64_t)gridDim.x;
-        const uint8_t* src = nullptr;
-        uint8_t* dst = nullptr;
-        uint32_t bytes = 0;
-        if (u < total) bytes = page_unit<MODE>(a, u, src, dst);
-        unsigned todo = __ballot_sync(FULL_MASK, bytes != 0);
-        while (todo) {
-            const W* from[2];
-            W* to[2];
-            uint32_t n[2];
+    } else {
+        for (int64_t base = blockIdx.x; base < total; base += 32 * (int64_t)gridDim.x) {
+            const int64_t u = base + lane * (int64_t)gridDim.x;
+            const uint8_t* src = nullptr;
+            uint8_t* dst = nullptr;
+            uint32_t bytes = 0;
+            if (u < total) bytes = page_unit<MODE>(a, u, src, dst);
+            unsigned todo = __ballot_sync(FULL_MASK, bytes != 0);
+            while (todo) {
+                const W* from[2];
+                W* to[2];
+                uint32_t n[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const int at = todo ? __ffs(todo) - 1 : 0;
-                from[k] = reinterpret_cast<const W*>(__shfl_sync(FULL_MASK, reinterpret_cast<uint64_t>(src), at));
-                to[k] = reinterpret_cast<W*>(__shfl_sync(FULL_MASK, reinterpret_cast<uint64_t>(dst), at));
-                n[k] = __shfl_sync(FULL_MASK, bytes, at) / sizeof(W);
-                if (!todo) n[k] = 0;
-                todo &= todo - 1;
-            }
-            if (sizeof(W) == 16) {
-                W x[2][PER];
+                for (int k = 0; k < 2; ++k) {
+                    const int at = todo ? __ffs(todo) - 1 : 0;
+                    from[k] = reinterpret_cast<const W*>(__shfl_sync(FULL_MASK, reinterpret_cast<uint64_t>(src), at));
+                    to[k] = reinterpret_cast<W*>(__shfl_sync(FULL_MASK, reinterpret_cast<uint64_t>(dst), at));
+                    n[k] = __shfl_sync(FULL_MASK, bytes, at) / sizeof(W);
+                    if (!todo) n[k] = 0;
+                    todo &= todo - 1;
+                }
+                if (sizeof(W) == 16) {
+                    W x[2][PER];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int q = 0; q < PER; ++q)
-                        if (threadIdx.x + q * PG_THREADS < n[k]) x[k][q] = from[k][threadIdx.x + q * PG_THREADS];
+                        for (int q = 0; q < PER; ++q)
+                            if (threadIdx.x + q * PG_THREADS < n[k]) x[k][q] = from[k][threadIdx.x + q * PG_THREADS];
 #pragma unroll
-                for (int k = 0; k < 2; ++k)
+                    for (int k = 0; k < 2; ++k)
 #pragma unroll
-                    for (int q = 0; q < PER; ++q)
-                        if (threadIdx.x + q * PG_THREADS < n[k]) to[k][threadIdx.x + q * PG_THREADS] = x[k][q];
-            } else {
-                for (int k = 0; k < 2; ++k)
-                    for (uint32_t i = threadIdx.x; i < n[k]; i += PG_THREADS) to[k][i] = from[k][i];
+                        for (int q = 0; q < PER; ++q)
+                            if (threadIdx.x + q * PG_THREADS < n[k]) to[k][threadIdx.x + q * PG_THREADS] = x[k][q];
+                } else {
+                    for (int k = 0; k < 2; ++k)
+                        for (uint32_t i = threadIdx.x; i < n[k]; i += PG_THREADS) to[k][i] = from[k][i];
+                }
             }
         }
     }
@@ -297,6 +297,7 @@ __device__ __forceinline__ int block_scan(int v, int* sum, int* warp_sums) {
 // the same child the first is taken (a minimum over claims left in the row's
 // length, so the answer does not depend on timing), and a row may not be a
 // parent and a child of one call.
+// A few microseconds: chains of dependent loads, not work.
 // fresh[i]: the page to copy the parent's last page into, -1 (whole pages
 // only: nothing to copy), or -2 (refused).
 // ---------------------------------------------------------------------------
@@ -394,7 +395,7 @@ __global__ void __launch_bounds__(PL_THREADS) fork_plan_kernel(const ForkArgs a)
 // U stay; the others, in ascending order, take the holes below U, in ascending
 // order, so that as few pages as possible move and no page is both a source
 // and a destination.
-// One CTA; a thread takes a stretch of consecutive pages, so that three scans
+// One CTA (8192 pages in 10 us, latency); a thread takes a stretch of consecutive pages, so that three scans
 // over the threads' counts order everything.  The list of holes stands at
 // page_map[U + i] until the page that takes hole i, which is at U + i or
 // above, overwrites it: the pages above U go through the list from the last
@@ -414,7 +415,9 @@ __global__ void __launch_bounds__(PL_THREADS) compact_plan_kernel(const CompactA
     pdl_trigger();
     const int len = (n + PL_THREADS - 1) / PL_THREADS, p0 = min(tid * len, n), p1 = min(p0 + len, n);
     int mine = 0, used, unused;
-    for (int p = p0; p < p1; ++p) mine += a.ref_count[p] > 0;
+    // (the count of all does not care who reads which page: neighbours for neighbours, loads ahead)
+#pragma unroll 8
+    for (int p = tid; p < n; p += PL_THREADS) mine += a.ref_count[p] > 0;
     block_scan(mine, &used, warp_sums);
     // the holes below U, and the pages that stay
     const int q1 = min(p1, used);
@@ -440,11 +443,22 @@ __global__ void __launch_bounds__(PL_THREADS) compact_plan_kernel(const CompactA
         below -= cnt;
     }
     __syncthreads();
-    for (int p = tid; p < n; p += PL_THREADS) {
-        const int to = __ldcg(a.page_map + p);
-        const int r = a.ref_count[p];
-        if (to >= 0) a.new_ref[to] = r;
-        if (p >= used) a.new_ref[p] = 0;
+    for (int q = tid; q < n; q += 4 * PL_THREADS) {
+        int to[4], r[4];
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const int p = q + z * PL_THREADS;
+            to[z] = p < n ? __ldcg(a.page_map + p) : -1;
+            r[z] = p < n ? a.ref_count[p] : 0;
+        }
+        // in place: a page's new place below U was a hole, or the page itself, so no count that is still
+        // to be read is written here
+#pragma unroll
+        for (int z = 0; z < 4; ++z) {
+            const int p = q + z * PL_THREADS;
+            if (to[z] >= 0) a.new_ref[to[z]] = r[z];
+            if (p < n && p >= used) a.new_ref[p] = 0;
+        }
     }
 }
 

@@ -126,6 +126,11 @@ __device__ __forceinline__ void tm_st16(uint32_t t, const uint32_t (&r)[16]) {
         : "memory");
 }
 
+// fetch a tensor map ahead of its first use
+__device__ __forceinline__ void tma_prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(reinterpret_cast<uint64_t>(map)) : "memory");
+}
+
 // 3-D tiled TMA load of box {x, y, z} (x innermost) into this CTA's shared memory
 __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, int32_t x, int32_t y, int32_t z,
                                             uint64_t* bar) {
