@@ -45,8 +45,8 @@ struct SeqSpan {
 };
 
 // Sequence b's rows; an offset outside [0, T] or a negative length sets
-// FAULT_SLOT_RANGE (if `report`) and the sequence counts as empty.
-__device__ __forceinline__ SeqSpan prompt_span(const PromptArgs& a, int b, bool report) {
+// FAULT_SLOT_RANGE and the sequence counts as empty.
+__device__ __forceinline__ SeqSpan prompt_span(const PromptArgs& a, int b) {
     SeqSpan s;
     if (a.cu_q == nullptr) {
         s.q0 = (int64_t)b * a.S;
@@ -54,7 +54,7 @@ __device__ __forceinline__ SeqSpan prompt_span(const PromptArgs& a, int b, bool 
     } else {
         const int32_t lo = __ldg(a.cu_q + b), hi = __ldg(a.cu_q + b + 1);
         const bool ok = lo >= 0 && hi >= lo && hi <= a.T;
-        if (!ok && report) raise_fault(FAULT_SLOT_RANGE);
+        if (!ok) raise_fault(FAULT_SLOT_RANGE);
         s.q0 = ok ? lo : 0;
         s.lq = ok ? hi - lo : 0;
     }
@@ -64,7 +64,7 @@ __device__ __forceinline__ SeqSpan prompt_span(const PromptArgs& a, int b, bool 
     } else {
         const int32_t lo = __ldg(a.cu_k + b), hi = __ldg(a.cu_k + b + 1);
         const bool ok = lo >= 0 && hi >= lo && hi <= a.Tk;
-        if (!ok && report) raise_fault(FAULT_SLOT_RANGE);
+        if (!ok) raise_fault(FAULT_SLOT_RANGE);
         s.k0 = ok ? lo : 0;
         s.lk = ok ? hi - lo : 0;
         if (!ok) s.lq = 0;

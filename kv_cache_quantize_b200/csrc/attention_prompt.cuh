@@ -160,7 +160,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                 int32_t nt = 0;
                 SeqSpan s = {0, 0, 0, 0};
                 if (b < a.B) {
-                    s = prompt_span(a, b, true);
+                    s = prompt_span(a, b);
                     nt = (s.lq + 2 * TOK - 1) / (2 * TOK);
                 }
                 int32_t incl = nt;
