@@ -241,7 +241,8 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     ++pos;
                     return true;
                 };
-                dead = !load_q(0) || (n > 0 && !load_kv(&tm_k, 0)) || !load_q(1) || (n > 0 && !load_kv(&tm_v, 0));
+                // the first keys and values need only room in the ring; Q waits for the item before
+                dead = (n > 0 && (!load_kv(&tm_k, 0) || !load_kv(&tm_v, 0))) || !load_q(0) || !load_q(1);
                 for (int j = 1; j < n && !dead; ++j) dead = !load_kv(&tm_k, j) || !load_kv(&tm_v, j);
             }
             dead = __shfl_sync(FULL_MASK, dead, 0);
