@@ -140,7 +140,7 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
         // ---------------- work items and loads ----------------
         asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
         const uint32_t q_bytes = (uint32_t)(TOK * a.G) * 128u * PANELS;
-        uint32_t pos = 0, n_item = 0, n_asked = 0, q_n[2] = {0, 0};
+        uint32_t pos = 0, n_item = 0, n_asked = 0, n_answered = 0, q_n[2] = {0, 0};
         int cb = 0;
         int64_t cbase = 0;                                   // tiles of the sequences before cb
         bool dead = false;
@@ -184,7 +184,10 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
                     cb += 32;
                 }
             }
-            if (it >= 0 && lane == 0) take_over(taken, next_item);
+            if (it >= 0) {
+                if (lane == 0) take_over(taken, next_item);
+                ++n_asked;
+            }
             PromptItem w;
             w.n0 = -1;
             w.n1 = 0;
@@ -247,13 +250,14 @@ __global__ void __launch_bounds__(PA_THREADS, 1)
             }
             dead = __shfl_sync(FULL_MASK, dead, 0);
             // the answer to the request is there by now
-            if (!__all_sync(FULL_MASK, mbar_wait_ns(next_item, n_asked++ & 1u, PA_WAIT_NS))) break;
+            if (!__all_sync(FULL_MASK, mbar_wait_ns(next_item, n_answered++ & 1u, PA_WAIT_NS))) break;
             it = taken_over(taken);
             __syncwarp();
             fence_proxy_async_smem();                        // read before the next answer is written
         }
-        // no load may still be in flight when the CTA exits
+        // no load, and no answer, may still be in flight when the CTA exits
         if (lane == 0) {
+            if (n_answered < n_asked) mbar_wait_ns(next_item, n_answered & 1u, PA_WAIT_NS);
             for (int i = 0; i < 2; ++i)
                 if (q_n[i] > 0) mbar_wait_ns(&q_full[i], (q_n[i] - 1) & 1u, PA_WAIT_NS);
             for (uint32_t k = pos > NS ? pos - NS : 0; k < pos; ++k)
