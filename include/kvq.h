@@ -330,7 +330,10 @@ KVQ_API kvq_status kvq_compressor(const kvq_tensor* x, const kvq_tensor* w_kv, c
 /* Per row: out = sum_j softmax_j(softmax_scale * q . k_j) v_j.  A row that   */
 /* sees no key: out 0, lse -inf.  Scores, maxima, sums and the output         */
 /* accumulate in fp32; the weights are rounded to q's type for the product    */
-/* with v.  One kernel on `stream`; nothing is allocated; no workspace.       */
+/* with v.  A value of v that is infinite makes its channel infinite in every */
+/* row that sees it, or NaN where the row's weight of it may round to 0 (2^-33 */
+/* of the row's largest for f16, 2^-126 for bf16); no other row is touched.   */
+/* One kernel on `stream`; nothing is allocated; no workspace.                */
 /* ------------------------------------------------------------------------ */
 KVQ_API kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k, const kvq_tensor* v,
                                         const kvq_tensor* cu_seqlens_q, const kvq_tensor* cu_seqlens_k,

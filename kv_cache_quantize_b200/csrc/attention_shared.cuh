@@ -22,7 +22,9 @@
 // one warp of each tile to go through 128 keys alone, some 2600 cycles: its
 // rows stand four times in the tile, at lanes 0, 32, 64 and 96, and the warp of
 // each copy takes 32 of the step's keys, its weights of the others being zero.
-// The four are pieces of their own for the join.
+// The four are pieces of their own for the join.  Zero times an infinite value
+// is NaN: a copy whose output holds NaN puts those channels right at its end
+// from the values themselves (16-bit caches; int8 codes are finite).
 //
 // Q has two buffers.  A piece of two tiles of rows fills both; others use them
 // in turn, one for both tiles, so that the next piece's Q is in place before
@@ -909,6 +911,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             w.b0 = items[slot].b0;
             w.nreq = items[slot].nreq;
             w.kh = items[slot].kh;
+            w.key0 = items[slot].key0;
             w.keys = items[slot].keys;
             w.slot = items[slot].slot;
             __syncwarp();
@@ -1080,14 +1083,57 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 const int tile_rows = w.own ? plan.own_rows : plan.tile_rows;
                 const int64_t row = ((int64_t)w.slot * 2 + i) * tile_rows + (w.narrow ? (warp & 3) * rows : 0) + lr;
                 float* o_out = ws + (w.own ? plan.own_area : 0) + row * D;
+                float any_nan = 0.0f;                        // NaN once a value is
 #pragma unroll 1
                 for (int k = 0; k < D; k += 32) {
                     uint32_t o[32];
                     tm_ld32(o_t + k, o);
+                    if (!I8) {
+#pragma unroll
+                        for (int q = 0; q < 32; q += 2) any_nan = max3(any_nan, __uint_as_float(o[q]), __uint_as_float(o[q + 1]));
+                    }
                     if (live) {
 #pragma unroll
                         for (int q = 0; q < 8; ++q)
                             reinterpret_cast<uint4*>(o_out + k)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
+                    }
+                }
+                // (a row whose sum is NaN stays NaN whatever is done here)
+                if (!I8 && w.narrow && __any_sync(FULL_MASK, live && any_nan != any_nan && l == l)) {
+                    // The copies' zero weights met values of V that are not finite (0 * Inf is NaN).  Every row of
+                    // the piece sees those values, so where one stands the joined channel is the sum of such
+                    // values alone: this copy's part of it is the sum over its own 32 keys of each step, 0 if
+                    // they hold none.  A lane looks at one channel of all keys.
+                    const int32_t* list = w.own ? a.table + (int64_t)w.b0 * a.table_stride : a.prefix_table;
+#pragma unroll 1
+                    for (int k = 0; k < D; k += 32) {
+                        float own = 0.0f;
+                        bool odd = false;
+#pragma unroll 1
+                        for (int s = first; s < w.steps; s += stride) {
+                            const int n = min(w.keys - s * SA_KEYS, SA_KEYS);
+#pragma unroll 4
+                            for (int t = 0; t < n; ++t) {
+                                const uint32_t tok = (uint32_t)(w.key0 + s * SA_KEYS + t);
+                                const uint32_t e = a.block_shift >= 0 ? tok >> a.block_shift : tok / (uint32_t)a.block;
+                                const int32_t page = list[e];
+                                if ((uint32_t)page >= (uint32_t)a.num_pages) continue;
+                                const int64_t v = ((int64_t)(tok - e * (uint32_t)a.block) * a.Nkv + w.kh) * D + k + lane;
+                                const float x = att_load<T>(a.v_cache + (int64_t)page * a.page_bytes, v);
+                                if (fabsf(x) < INFINITY) continue;
+                                odd = true;
+                                if ((t >> 5) == (warp & 3)) own = __fadd_rn(own, x);
+                            }
+                        }
+                        const unsigned odds = __ballot_sync(FULL_MASK, odd);
+                        uint32_t o[32];
+                        __syncwarp();
+                        tm_ld32(o_t + k, o);
+#pragma unroll
+                        for (int q = 0; q < 32; ++q) {
+                            const float x = __shfl_sync(FULL_MASK, own, q), y = __uint_as_float(o[q]);
+                            if (live && (odds >> q & 1u) && y != y) o_out[k + q] = x;
+                        }
                     }
                 }
                 if (live) {
