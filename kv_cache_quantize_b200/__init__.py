@@ -359,12 +359,14 @@ def _calls():
 
 
 def _done(op: str, answer, check: bool):
-    """The result of a call, or its error: (status, stream, result)."""
-    status, stream, result = answer
+    """The result of a call, or its error: (status, stream, device, result).  A fault word is a device's own, and a
+    stream handle means nothing on another one: the check runs on the call's device (-1: all tensors were empty)."""
+    status, stream, device, result = answer
     if status:
         raise KvqError(op, status)
     if check:
-        _faults(op, True, stream)
+        with _on(torch.device("cuda", device) if device >= 0 else None):
+            _faults(op, True, stream)
     return result
 
 

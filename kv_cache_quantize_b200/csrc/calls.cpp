@@ -109,7 +109,8 @@ struct Call {
     }
 
     // Run `f(stream)` with the device current; None: the device's current
-    // stream (the legacy default one where every tensor is empty).
+    // stream (the legacy default one where every tensor is empty).  Returns
+    // (status, stream, device or -1, result).
     template <typename F>
     PyObject* run(PyObject* stream, PyObject* result, F f) {
         void* s = nullptr;
@@ -126,8 +127,7 @@ struct Call {
         st = f(reinterpret_cast<kvq_stream>(s));
         Py_END_ALLOW_THREADS
         PyObject* stream_int = PyLong_FromVoidPtr(s);
-        PyObject* ret = Py_BuildValue("(iNO)", (int)st, stream_int, result);
-        return ret;
+        return Py_BuildValue("(iNiO)", (int)st, stream_int, device, result);
     }
 };
 

@@ -1,0 +1,62 @@
+"""The binding of the attention and page calls without a GPU: what it does around the library's calls."""
+import contextlib
+import ctypes
+
+import pytest
+import torch
+
+import kv_cache_quantize_b200 as kvq
+
+
+class Extension:
+    """Stands in for the extension module: every call ran on device 1, its default stream."""
+
+    def __getattr__(self, name):
+        return lambda *args: (0, 0, 1, name)
+
+
+class Library:
+    """Stands in for the library: get_error answers from the fault word of the device that is current."""
+
+    def __init__(self):
+        self.current, self.words = 0, {0: kvq.FAULT_TIMEOUT, 1: kvq.FAULT_NO_PAGE}
+
+    def kvq_get_error(self, stream, bits):
+        ctypes.cast(bits, ctypes.POINTER(ctypes.c_uint32))[0] = self.words[self.current]
+        self.words[self.current] = 0
+        return 0
+
+
+E = torch.empty((0,), dtype=torch.int32)
+CALLS = {"prompt_attention": (E, E, E), "shared_prefix_attention": (E, E, E, E, E), "copy_pages": ([E], E, E),
+         "free_pages": (E, E, E, E, 16), "fork_pages": ([E], E, E, E, E, E, 16), "compact_pages": ([E], E, E)}
+
+
+@pytest.mark.parametrize("name", CALLS)
+def test_check_reads_the_fault_word_of_the_calls_device(name, monkeypatch):
+    """Tensors on device 1 while device 0 is current: the fault of device 1 is raised, that of device 0 stays."""
+    library = Library()
+
+    @contextlib.contextmanager
+    def on(dev):
+        before, library.current = library.current, library.current if dev is None else dev.index
+        yield
+        library.current = before
+
+    monkeypatch.setattr(kvq, "_calls", Extension)
+    monkeypatch.setattr(kvq, "lib", lambda: library)
+    monkeypatch.setattr(kvq, "_on", on)
+    call = getattr(kvq, name)
+    assert call(*CALLS[name]) in (name, None)
+    with pytest.raises(kvq.KvqFault) as e:
+        call(*CALLS[name], check=True)
+    assert e.value.args and "FAULT_NO_PAGE" in str(e.value)
+    assert library.words == {0: kvq.FAULT_TIMEOUT, 1: 0}
+    assert call(*CALLS[name], check=True) in (name, None)
+
+
+def test_calls_answer_with_their_device():
+    """Where every tensor is empty there is none."""
+    c = torch.empty((0, 4), dtype=torch.int8)
+    status, stream, device, result = kvq._calls().copy_pages([c], E, E, None)
+    assert (status, stream, device, result) == (0, 0, -1, None)

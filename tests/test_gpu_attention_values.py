@@ -105,3 +105,10 @@ def test_values_that_are_not_finite_beside_pages_that_are_not_there():
     pages[1] = torch.where(torch.isfinite(pages[1].float()), pages[1], 0)
     want, _, bound, _ = shared64(d["q"][:1], *pages, table, lens, None, 0)
     check_rows(out[:1], torch.where(reached, math.nan, want), bound)
+
+
+def test_calls_answer_with_their_device():
+    d = paged(46, [5], 0, 8, 2, 64, 16, BF, BF)
+    page = torch.zeros((1,), dtype=torch.int32, device="cuda")
+    answer = kvq._calls().copy_pages([d["kc"]], page, page, None)
+    assert answer[0] == 0 and answer[2] == d["kc"].get_device()
