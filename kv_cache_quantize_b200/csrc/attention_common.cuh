@@ -16,6 +16,12 @@ constexpr float ATT_LOG2E = 1.4426950408889634f;
 constexpr float ATT_F16_SHIFT = 8.0f;
 constexpr float ATT_LN2 = 0.6931471805599453f;
 
+// What a kernel of this library may have written just before (queries, tables,
+// lengths, offsets of sequences, caches) is read by plain loads: the kernels
+// start while the one before them may still run (pdl_wait), and the read-only
+// path (__ldg) is for data that nobody writes meanwhile, the caches' scales and
+// offsets.
+
 // element types of queries, outputs and 16-bit caches; ATT_I8: int8 caches
 enum { ATT_BF16 = 0, ATT_F16 = 1, ATT_I8 = 2 };
 
@@ -52,7 +58,7 @@ __device__ __forceinline__ SeqSpan prompt_span(const PromptArgs& a, int b) {
         s.q0 = (int64_t)b * a.S;
         s.lq = a.S;
     } else {
-        const int32_t lo = __ldg(a.cu_q + b), hi = __ldg(a.cu_q + b + 1);
+        const int32_t lo = a.cu_q[b], hi = a.cu_q[b + 1];
         const bool ok = lo >= 0 && hi >= lo && hi <= a.T;
         if (!ok) raise_fault(FAULT_SLOT_RANGE);
         s.q0 = ok ? lo : 0;
@@ -62,7 +68,7 @@ __device__ __forceinline__ SeqSpan prompt_span(const PromptArgs& a, int b) {
         s.k0 = (int64_t)b * a.Sk;
         s.lk = a.Sk;
     } else {
-        const int32_t lo = __ldg(a.cu_k + b), hi = __ldg(a.cu_k + b + 1);
+        const int32_t lo = a.cu_k[b], hi = a.cu_k[b + 1];
         const bool ok = lo >= 0 && hi >= lo && hi <= a.Tk;
         if (!ok) raise_fault(FAULT_SLOT_RANGE);
         s.k0 = ok ? lo : 0;
@@ -96,7 +102,7 @@ struct SharedArgs {
 // Request b's own length: -1 for a row that takes no part; a length that its
 // table row cannot hold sets FAULT_SLOT_RANGE and counts as -1.
 __device__ __forceinline__ int32_t own_length(const SharedArgs& a, int b) {
-    const int32_t n = __ldg(a.seq_lens + b);
+    const int32_t n = a.seq_lens[b];
     if (n < -1 || n > (int64_t)a.cols * a.block) {
         raise_fault(FAULT_SLOT_RANGE);
         return -1;

@@ -128,7 +128,7 @@ __device__ __forceinline__ int64_t ceil_div(int64_t x, int k) {
 }
 
 __device__ __forceinline__ int32_t own_blocks(const SharedArgs& a, int b) {
-    const int32_t n = __ldg(a.seq_lens + b);
+    const int32_t n = a.seq_lens[b];
     return n > 0 && n <= (int64_t)a.cols * a.block ? (n + SA_KEYS - 1) / SA_KEYS : 0;
 }
 
@@ -297,7 +297,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             const int t = s * SA_KEYS + lane * box;
             const bool wanted = lane < pieces && t < keys;
             int32_t page = -1;
-            if (wanted) page = __ldg(list + ((key0 + t) >> a.block_shift));
+            if (wanted) page = list[(key0 + t) >> a.block_shift];
             const bool there = (uint32_t)page < (uint32_t)a.num_pages;
             const unsigned got = __ballot_sync(FULL_MASK, there), lost = __ballot_sync(FULL_MASK, wanted && !there);
             const uint32_t st = I8 ? tile_no % NR : tile_no % NS, turn = I8 ? tile_no / NR : tile_no / NS;
@@ -376,8 +376,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 const int lr = r0 + z * RPP + lane / LPR;
                 const int b = b0 + (own ? 0 : lr / a.G), h = kh * a.G + (own ? lr : lr % a.G);
                 const uint4* q = reinterpret_cast<const uint4*>(a.q.base + ((int64_t)b * a.q.tok + h * a.q.head + c16) * 2);
-                e[z][0] = lr < end ? __ldg(q) : make_uint4(0u, 0u, 0u, 0u);
-                e[z][1] = lr < end ? __ldg(q + 1) : make_uint4(0u, 0u, 0u, 0u);
+                e[z][0] = lr < end ? q[0] : make_uint4(0u, 0u, 0u, 0u);
+                e[z][1] = lr < end ? q[1] : make_uint4(0u, 0u, 0u, 0u);
             }
 #pragma unroll
             for (int u = 0; u < 4; ++u) {
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                     w.own = 1;
                     w.nreq = 1;
                     w.alt = 1;
-                    len = __ldg(a.seq_lens + w.b0);
+                    len = a.seq_lens[w.b0];
                     w.slot = w.b0 * a.Nkv;
                 }
                 const int64_t cost = (int64_t)k * blocks;
@@ -834,7 +834,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 if (t >= keys) return 0xFFFFFFFFu;
                 const uint32_t tok = (uint32_t)(key0 + t);
                 const uint32_t e = a.block_shift >= 0 ? tok >> a.block_shift : tok / (uint32_t)a.block;
-                const int32_t page = __ldg(list + e);
+                const int32_t page = list[e];
                 const uint32_t in = (tok - e * (uint32_t)a.block) * row_units;
                 return (uint32_t)page < (uint32_t)a.num_pages ? (uint32_t)page * page_units + in : 0xFFFFFFFFu;
             };
