@@ -381,7 +381,14 @@ KVQ_API kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_te
                                                float softmax_scale, kvq_tensor* workspace, kvq_stream stream);
 
 /* Bytes of workspace of a call with these sizes (max_own: cols * block of the
- * block table), or -1 for sizes the call refuses. */
+ * block table), or -1 for sizes the call refuses.  With G = n_q / n_kv, it is
+ * about 4 (dim + 2) bytes for each of
+ *   own keys  (batch * n_kv + 148) * r rows, r = 0 for max_own 0, 4 G (G > 32:
+ *             G) up to 128, twice that beyond;
+ *   prefix    (batch * n_q / 128 + 148) * 256 rows, fewer for a batch of one
+ *             tile; none for prefix_len 0:
+ * 548 MB for 4096 requests with 32 / 8 heads of 128 and long lists of their
+ * own, half of it where cols * block is 128. */
 KVQ_API int64_t kvq_shared_prefix_attention_workspace(int64_t batch, int64_t n_q, int64_t n_kv, int64_t dim,
                                                       int64_t prefix_len, int64_t max_own);
 

@@ -88,8 +88,10 @@ kvq_status run_prompt(const PromptArgs& a, cudaStream_t s) {
 
 // How the work is laid out, and the workspace in bytes.  The size is that of
 // two-tile groups in either form (a one-tile group needs half the rows, twice
-// the groups), for as many CTAs as the kernel ever has.
-int64_t shared_plan(int64_t B, int64_t Nq, int64_t Nkv, int64_t D, int64_t prefix_len, bool hilo, SharedPlan* p) {
+// the groups), for as many CTAs as the kernel ever has, and for requests of up
+// to max_own own tokens: a list of one step only ever uses the first tile.
+int64_t shared_plan(int64_t B, int64_t Nq, int64_t Nkv, int64_t D, int64_t prefix_len, int64_t max_own, bool hilo,
+                    SharedPlan* p) {
     const int64_t G = Nq / Nkv, tok = 128 / G;
     auto area = [&](int64_t group, int64_t* slots, int64_t* rows) {
         *slots = prefix_len > 0 ? ((B + group - 1) / group) * Nkv + SA_MAX_CTAS : 0;
@@ -102,7 +104,8 @@ int64_t shared_plan(int64_t B, int64_t Nq, int64_t Nkv, int64_t D, int64_t prefi
     const int64_t pre = area(tok, &slots, &rows);                   // rows of the prefix slots, the larger form
     area(group, &slots, &rows);
     p->own_rows = (int32_t)(G <= 32 ? 4 * G : G);
-    const int64_t own = (B * Nkv + SA_MAX_CTAS) * 2 * p->own_rows;
+    p->own_slot = max_own == 0 ? 0 : max_own <= SA_KEYS ? p->own_rows : 2 * p->own_rows;
+    const int64_t own = (B * Nkv + SA_MAX_CTAS) * p->own_slot;
     p->group = (int32_t)group;
     p->n_groups = (int32_t)((B + group - 1) / group);
     p->blocks = (int32_t)((prefix_len + SA_KEYS - 1) / SA_KEYS);
@@ -140,7 +143,7 @@ template <int T, int C, int D>
 kvq_status run_shared(const SharedArgs& a, cudaStream_t s) {
     constexpr bool I8 = C == ATT_I8;
     SharedPlan p;
-    shared_plan(a.B, a.Nq, a.Nkv, D, a.prefix_len, I8 && T == ATT_F16, &p);
+    shared_plan(a.B, a.Nq, a.Nkv, D, a.prefix_len, (int64_t)a.cols * a.block, I8 && T == ATT_F16, &p);
     p.cost_own = I8 ? SA_COST_OWN8 : SA_COST_OWN16;
     CUtensorMap mq = {}, mq1 = {};
     if (!I8 && (!rows_map(&mq, T, a.q, a.B, a.Nq, D, a.G, 128 / a.G) || !rows_map(&mq1, T, a.q, a.B, a.Nq, D, a.G, a.G <= 32 ? 32 / a.G : 1)))
@@ -246,7 +249,7 @@ int64_t kvq_shared_prefix_attention_workspace(int64_t batch, int64_t n_q, int64_
         prefix_len < 0 || max_own < 0 || batch > ATT_MAX_TOKENS / n_q || max_own + prefix_len > ATT_MAX_TOKENS)
         return -1;
     SharedPlan p;
-    return shared_plan(batch, n_q, n_kv, dim, prefix_len, false, &p);
+    return shared_plan(batch, n_q, n_kv, dim, prefix_len, max_own, false, &p);
 }
 
 kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_cache, const kvq_tensor* v_cache,

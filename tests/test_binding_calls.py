@@ -60,3 +60,16 @@ def test_calls_answer_with_their_device():
     c = torch.empty((0, 4), dtype=torch.int8)
     status, stream, device, result = kvq._calls().copy_pages([c], E, E, None)
     assert (status, stream, device, result) == (0, 0, -1, None)
+
+
+def test_workspace_follows_the_own_keys_a_call_can_have():
+    """No own keys: no room for them.  One step of 128 keys: one tile's rows.  More: two tiles'."""
+    f = kvq.shared_prefix_attention_workspace
+    for args in ((2048, 64, 8, 128), (3, 12, 3, 64), (64, 128, 1, 128), (1, 40, 1, 64)):
+        none, one, full, more = (f(*args, 4096, own) for own in (0, 128, 129, 1 << 20))
+        assert 0 < none < one < full == more and f(*args, 4096, 1) == one
+        b, nq, nkv, d = args
+        rows = 4 * nq // nkv if nq // nkv <= 32 else nq // nkv
+        assert one - none == full - one == (b * nkv + 148) * rows * (d + 2) * 4
+        assert f(*args, 0, 0) == 4 * (b + 1) + f(0, *args[1:], 0, 0) - 4
+    assert f(256, 16, 4, 128, 32768, 1024) > 0

@@ -112,3 +112,27 @@ def test_calls_answer_with_their_device():
     page = torch.zeros((1,), dtype=torch.int32, device="cuda")
     answer = kvq._calls().copy_pages([d["kc"]], page, page, None)
     assert answer[0] == 0 and answer[2] == d["kc"].get_device()
+
+
+@pytest.mark.parametrize("heads", [(8, 2), (40, 1)])
+@pytest.mark.parametrize("dtype,cache", [(BF, torch.int8), (F16, torch.int8), (F16, F16)])
+@pytest.mark.parametrize("cols", [0, 1, 8, 9, 20])
+def test_workspace_of_just_the_size_that_is_asked_for(cols, dtype, cache, heads):
+    """Tables without columns, of one step of 128 keys and of more; the bytes behind the workspace stay as they are,
+    and what stood in it (NaN) does not matter."""
+    for batch, prefix in ((5, 300), (150, 1000), (3, 0)):
+        lens = [min(cols * 16, i * 29 % (cols * 16 + 1) + (i % 3 == 0) * 40) for i in range(batch)]
+        d = paged(47, lens, prefix, *heads, 64, 16, dtype, cache)
+        d["table"] = d["table"][:, :cols] if cols <= d["table"].shape[1] else torch.nn.functional.pad(
+            d["table"], (0, cols - d["table"].shape[1]), value=-1)
+        assert d["table"].shape == (batch, cols)
+        want, wl, bound, lb = want_shared(d)
+        need = kvq.shared_prefix_attention_workspace(batch, *heads, 64, prefix, cols * 16)
+        ws = torch.full((need + 4096,), 0xFF, dtype=torch.uint8, device="cuda")
+        lse = torch.zeros((batch, heads[0]), dtype=torch.float32, device="cuda")
+        out = call_shared(d, workspace=ws[:need], lse=lse, check=True)
+        check_rows(out, want, bound, "out")
+        check_rows(lse, wl, lb, "lse")
+        assert bool((ws[need:] == 0xFF).all())
+        with pytest.raises(kvq.KvqError):
+            call_shared(d, workspace=ws[:need - 1])
