@@ -321,7 +321,8 @@ KVQ_API kvq_status kvq_compressor(const kvq_tensor* x, const kvq_tensor* w_kv, c
 /*          keep their contents.  A span that is negative or not inside the   */
 /*          tensor counts as an empty sequence and sets KVQ_FAULT_SLOT_RANGE  */
 /*          (rows of other sequences may then be left unwritten where the     */
-/*          offsets make them overlap).                                        */
+/*          offsets make them overlap).  Nkv (B + T / (2 floor(128 / G))) is    */
+/*          below 2^31 (G = Nq / Nkv).                                         */
 /* causal   nonzero: query i of a sequence with lq queries and lk keys sees   */
 /*          the keys j <= i + lk - lq (its own token is the last one it sees, */
 /*          also behind a cached context); 0: every key of the sequence.      */

@@ -68,6 +68,9 @@ bool rows_map(CUtensorMap* m, int type, const AttnRows& r, int64_t tokens, int64
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// at least the number of work items: pairs of tiles of each sequence and key head
+int64_t prompt_items(const PromptArgs& a) { return (a.T / (2 * (128 / a.G)) + a.B) * a.Nkv; }
+
 template <int T, int D>
 kvq_status run_prompt(const PromptArgs& a, cudaStream_t s) {
     const int tok = 128 / a.G;
@@ -79,11 +82,10 @@ kvq_status run_prompt(const PromptArgs& a, cudaStream_t s) {
     if (!rows_map(&mq, T, a.q, a.T, a.Nq, D, a.G, tok) || !rows_map(&mk, T, k, tk, nkv, D, 1, PA_KEYS) ||
         !rows_map(&mv, T, v, tk, nkv, D, 1, PA_KEYS))
         return KVQ_ERR_CUDA;
-    const int64_t items = (a.T / (2 * tok) + a.B) * a.Nkv;       // at least the number of work items
     auto kernel = prompt_kernel<T, D>;
     constexpr uint32_t smem = pa_smem_bytes(D);
     resident_blocks(reinterpret_cast<const void*>(kernel), PA_THREADS, smem);    // raises the shared-memory limit once
-    return launched(launch(kernel, (unsigned)items, PA_THREADS, smem, s, mq, mk, mv, a));
+    return launched(launch(kernel, (unsigned)prompt_items(a), PA_THREADS, smem, s, mq, mk, mv, a));
 }
 
 // How the work is laid out, and the workspace in bytes.  The size is that of
@@ -195,7 +197,7 @@ kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k, const 
     if (D != 64 && D != 128) return KVQ_ERR_UNSUPPORTED;
     if (Nkv < 1 || Nq < 1 || Nq % Nkv != 0) return KVQ_ERR_SHAPE;
     if (Nq / Nkv > 128) return KVQ_ERR_UNSUPPORTED;
-    if (a.T > ATT_MAX_TOKENS || a.Tk > ATT_MAX_TOKENS) return KVQ_ERR_SHAPE;
+    if (a.T > ATT_MAX_TOKENS || a.Tk > ATT_MAX_TOKENS || Nq > ATT_MAX_TOKENS) return KVQ_ERR_SHAPE;
     if (nd == 4) {
         if (k->shape[0] != q->shape[0] || v->shape[0] != q->shape[0] || v->shape[1] != k->shape[1] ||
             out->shape[0] != q->shape[0])
@@ -226,14 +228,15 @@ kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k, const 
         a.lse = static_cast<float*>(lse->data);
     }
     if (a.T == 0 || a.B == 0) return KVQ_OK;
+    a.Nq = (int32_t)Nq;
+    a.Nkv = (int32_t)Nkv;
+    a.G = (int32_t)(Nq / Nkv);
+    if (prompt_items(a) > INT32_MAX) return KVQ_ERR_SHAPE;      // a grid's CTAs
     if (!q->data || !out->data || (a.Tk > 0 && (!k->data || !v->data)) || (nd == 3 && (!a.cu_q || !a.cu_k)) ||
         (lse && !a.lse))
         return KVQ_ERR_NULL;
     if (!aligned16(q->data) || !aligned16(k->data) || !aligned16(v->data) || !aligned16(out->data))
         return KVQ_ERR_LAYOUT;
-    a.Nq = (int32_t)Nq;
-    a.Nkv = (int32_t)Nkv;
-    a.G = (int32_t)(Nq / Nkv);
     a.D = (int32_t)D;
     a.causal = causal != 0;
     a.out32 = reinterpret_cast<uintptr_t>(out->data) % 32 == 0 && a.out.tok % 16 == 0 && a.out.head % 16 == 0;

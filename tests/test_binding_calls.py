@@ -73,3 +73,36 @@ def test_workspace_follows_the_own_keys_a_call_can_have():
         assert one - none == full - one == (b * nkv + 148) * rows * (d + 2) * 4
         assert f(*args, 0, 0) == 4 * (b + 1) + f(0, *args[1:], 0, 0) - 4
     assert f(256, 16, 4, 128, 32768, 1024) > 0
+
+
+def descriptor(shape, dtype):
+    """With NULL data: a set that is accepted stops there (status 1) and reaches no launch."""
+    d = kvq.KvqTensor()
+    d.data, d.dtype, d.ndim = 0, kvq._DTYPES[dtype], len(shape)
+    stride = 1
+    for i in reversed(range(len(shape))):
+        d.shape[i], d.stride[i] = shape[i], stride
+        stride *= shape[i]
+    return d
+
+
+SHAPE, LAYOUT, NULL = 3, 6, 1
+
+
+@pytest.mark.parametrize("sequences,heads,status", [
+    ((1 << 29) + 7, 8, SHAPE),               # 2^32 + 56 work items, 56 in 32 bits
+    (1 << 29, 8, SHAPE), (1 << 28, 8, SHAPE), ((1 << 28) - 1, 8, NULL), (1 << 30, 1, NULL), ((1 << 30) - 1, 2, NULL), (4, 8, NULL)])
+def test_prompt_refuses_more_work_than_a_grid_holds(sequences, heads, status):
+    q = descriptor((50, heads, 64), torch.bfloat16)
+    cu = descriptor((sequences + 1 if sequences < 1 << 30 else 1 << 30,), torch.int32)
+    ref = lambda x: ctypes.addressof(x)  # noqa: E731
+    assert kvq.lib().kvq_prompt_attention(ref(q), ref(q), ref(q), ref(cu), None, ref(q), None, 1, 0.1, None) == status
+
+
+@pytest.mark.parametrize("heads,status", [((1 << 32) + 8, LAYOUT), ((1 << 31) + 8, SHAPE), ((1 << 30) + 8, SHAPE)])
+def test_prompt_refuses_more_heads_than_32_bits_hold(heads, status):
+    """The largest by its stride, 2^38 elements and more."""
+    q = descriptor((1, heads, 64), torch.bfloat16)
+    cu = descriptor((2,), torch.int32)
+    ref = lambda x: ctypes.addressof(x)  # noqa: E731
+    assert kvq.lib().kvq_prompt_attention(ref(q), ref(q), ref(q), ref(cu), None, ref(q), None, 1, 0.1, None) == status
