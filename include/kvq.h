@@ -357,6 +357,8 @@ KVQ_API kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k
 /*          caches.                                                            */
 /* block_table   int32 [B, cols], columns contiguous, any row stride (0 too): */
 /*          the pages of each request's own tokens, which follow the prefix.  */
+/*          cols * block + prefix_len at most 2^30, and B times the 128-token */
+/*          steps of cols * block below 2^31.                                  */
 /* seq_lens int32 [B]: own tokens of each request, 0 .. cols * block; -1: the */
 /*          row takes no part and its out and lse keep their contents.        */
 /* prefix_table  int32, at least ceil(prefix_len / block) pages (NULL when    */

@@ -88,6 +88,11 @@ kvq_status run_prompt(const PromptArgs& a, cudaStream_t s) {
     return launched(launch(kernel, (unsigned)prompt_items(a), PA_THREADS, smem, s, mq, mk, mv, a));
 }
 
+// the own steps of a batch are counted in 32 bits
+bool too_many_own_steps(int64_t batch, int64_t max_own) {
+    return batch * ((max_own + SA_KEYS - 1) / SA_KEYS) > INT32_MAX;
+}
+
 // How the work is laid out, and the workspace in bytes.  The size is that of
 // two-tile groups in either form (a one-tile group needs half the rows, twice
 // the groups), for as many CTAs as the kernel ever has, and for requests of up
@@ -249,7 +254,8 @@ kvq_status kvq_prompt_attention(const kvq_tensor* q, const kvq_tensor* k, const 
 int64_t kvq_shared_prefix_attention_workspace(int64_t batch, int64_t n_q, int64_t n_kv, int64_t dim,
                                               int64_t prefix_len, int64_t max_own) {
     if (batch < 0 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || n_q / n_kv > 128 || (dim != 64 && dim != 128) ||
-        prefix_len < 0 || max_own < 0 || batch > ATT_MAX_TOKENS / n_q || max_own + prefix_len > ATT_MAX_TOKENS)
+        prefix_len < 0 || max_own < 0 || batch > ATT_MAX_TOKENS / n_q || max_own > ATT_MAX_TOKENS ||
+        max_own + prefix_len > ATT_MAX_TOKENS || too_many_own_steps(batch, max_own))
         return -1;
     SharedPlan p;
     return shared_plan(batch, n_q, n_kv, dim, prefix_len, max_own, false, &p);
@@ -326,7 +332,9 @@ kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_
         if (!contiguous(prefix_table)) return KVQ_ERR_LAYOUT;
         a.prefix_table = static_cast<const int32_t*>(prefix_table->data);
     }
-    if (cols * block + prefix_len > ATT_MAX_TOKENS) return KVQ_ERR_SHAPE;
+    if (cols > ATT_MAX_TOKENS / block || cols * block + prefix_len > ATT_MAX_TOKENS ||
+        too_many_own_steps(B, cols * block))
+        return KVQ_ERR_SHAPE;
     if (!disjoint_rows(a.out, B, Nq, D)) return KVQ_ERR_LAYOUT;
     if (lse) {
         if (!valid_desc(lse) || lse->dtype != KVQ_F32) return KVQ_ERR_DTYPE;

@@ -106,3 +106,18 @@ def test_prompt_refuses_more_heads_than_32_bits_hold(heads, status):
     cu = descriptor((2,), torch.int32)
     ref = lambda x: ctypes.addressof(x)  # noqa: E731
     assert kvq.lib().kvq_prompt_attention(ref(q), ref(q), ref(q), ref(cu), None, ref(q), None, 1, 0.1, None) == status
+
+
+@pytest.mark.parametrize("batch,cols,status", [
+    (300, 1 << 19, SHAPE),                   # 300 x 2^23 steps of 128 keys, more than 2^31
+    (256, 1 << 19, SHAPE), (255, 1 << 19, NULL), (300, 1 << 12, NULL)])
+def test_shared_refuses_more_own_steps_than_32_bits_count(batch, cols, status):
+    """One table row for all requests (stride 0), pages of 2048 tokens."""
+    q, caches = descriptor((batch, 4, 64), torch.bfloat16), descriptor((8, 2048, 1, 64), torch.bfloat16)
+    table, lens, ws = descriptor((batch, cols), torch.int32), descriptor((batch,), torch.int32), descriptor((1 << 33,), torch.uint8)
+    table.stride[0] = 0
+    ref = lambda x: None if x is None else ctypes.addressof(x)  # noqa: E731
+    got = kvq.lib().kvq_shared_prefix_attention(*(ref(x) for x in (q, caches, caches, table, lens)), None, 0, None, None, None,
+                                                None, ref(q), None, 0.1, ref(ws), None)
+    assert got == status
+    assert (kvq.shared_prefix_attention_workspace(batch, 4, 1, 64, 0, cols * 2048) == -1) == (status == SHAPE)
