@@ -255,7 +255,7 @@ int64_t kvq_shared_prefix_attention_workspace(int64_t batch, int64_t n_q, int64_
                                               int64_t prefix_len, int64_t max_own) {
     if (batch < 0 || n_q < 1 || n_kv < 1 || n_q % n_kv != 0 || n_q / n_kv > 128 || (dim != 64 && dim != 128) ||
         prefix_len < 0 || max_own < 0 || batch > ATT_MAX_TOKENS / n_q || max_own > ATT_MAX_TOKENS ||
-        max_own + prefix_len > ATT_MAX_TOKENS || too_many_own_steps(batch, max_own))
+        prefix_len > ATT_MAX_TOKENS || max_own + prefix_len > ATT_MAX_TOKENS || too_many_own_steps(batch, max_own))
         return -1;
     SharedPlan p;
     return shared_plan(batch, n_q, n_kv, dim, prefix_len, max_own, false, &p);
@@ -324,6 +324,7 @@ kvq_status kvq_shared_prefix_attention(const kvq_tensor* q, const kvq_tensor* k_
     if (seq_lens->shape[0] != B) return KVQ_ERR_SHAPE;
     if (!contiguous(seq_lens)) return KVQ_ERR_LAYOUT;
     if (prefix_len < 0) return KVQ_ERR_ATTR;
+    if (prefix_len > ATT_MAX_TOKENS) return KVQ_ERR_SHAPE;
     if (prefix_len > 0) {
         if (!prefix_table) return KVQ_ERR_NULL;
         if (!valid_desc(prefix_table) || prefix_table->dtype != KVQ_I32) return KVQ_ERR_DTYPE;

@@ -121,3 +121,17 @@ def test_shared_refuses_more_own_steps_than_32_bits_count(batch, cols, status):
                                                 None, ref(q), None, 0.1, ref(ws), None)
     assert got == status
     assert (kvq.shared_prefix_attention_workspace(batch, 4, 1, 64, 0, cols * 2048) == -1) == (status == SHAPE)
+
+
+@pytest.mark.parametrize("prefix,status", [
+    ((1 << 63) - 1, SHAPE), ((1 << 63) - 1 - 0x7FFFFF00, SHAPE), ((1 << 32) + 5, SHAPE), ((1 << 30) + 1, SHAPE), (8 * 2048, NULL)])
+def test_shared_refuses_prefixes_whose_length_leaves_its_type(prefix, status):
+    """Lengths near 2^63 wrapped to small and negative ones, those above 2^31 lost their upper bits."""
+    q, caches = descriptor((2, 4, 64), torch.bfloat16), descriptor((8, 2048, 1, 64), torch.bfloat16)
+    table, lens, ws = descriptor((2, 3), torch.int32), descriptor((2,), torch.int32), descriptor((1 << 33,), torch.uint8)
+    pages = descriptor((8,), torch.int32)
+    ref = lambda x: None if x is None else ctypes.addressof(x)  # noqa: E731
+    got = kvq.lib().kvq_shared_prefix_attention(*(ref(x) for x in (q, caches, caches, table, lens, pages)), prefix, None, None,
+                                                None, None, ref(q), None, 0.1, ref(ws), None)
+    assert got == status
+    assert (kvq.shared_prefix_attention_workspace(2, 4, 1, 64, prefix, 3 * 2048) == -1) == (status == SHAPE)
