@@ -352,9 +352,14 @@ def _calls():
         if not os.path.exists(path):
             raise RuntimeError(f"extension not built: {path} is missing "
                                "(run `python -c 'import __graft_entry__ as g; g.build()'`)")
+        from . import build
+        if build.calls_torch() not in ("", build.installed_torch()):
+            raise RuntimeError(f"{path} was built for torch {build.calls_torch()}, installed is {build.installed_torch()} "
+                               "(run `python -c 'import __graft_entry__ as g; g.build()'`)")
         spec = importlib.util.spec_from_file_location("_calls", path)
-        _CALLS = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_CALLS)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+        _CALLS = module
     return _CALLS
 
 

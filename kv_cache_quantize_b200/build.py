@@ -6,6 +6,7 @@ binary32 multiply and add separately rounded (the kernels also use the
 explicitly rounded intrinsics); the CUDA runtime is linked statically so the
 library only needs the driver.
 """
+import importlib.metadata
 import os
 import re
 import shutil
@@ -20,6 +21,7 @@ LIB = os.path.join(HERE, "libkvq.so")
 OBJ = os.path.join(HERE, "_build")
 CALLS = os.path.join(HERE, "_calls.so")
 CALLS_SOURCE = os.path.join(CSRC, "calls.cpp")
+CALLS_TORCH = os.path.join(OBJ, "calls.torch")       # the torch and Python that _calls.so was built for
 CXX = os.environ.get("CXX", "g++")
 SOURCES = [os.path.join(CSRC, f) for f in ("kvq.cu", "attention.cu", "pages.cu")]
 NVCC = os.environ.get("NVCC", "nvcc")
@@ -46,9 +48,24 @@ def _stale(target, deps) -> bool:
     return not os.path.exists(target) or any(os.path.getmtime(p) > os.path.getmtime(target) for p in deps)
 
 
+def installed_torch() -> str:
+    return f"{importlib.metadata.version('torch')} {sys.implementation.cache_tag}"
+
+
+def calls_torch() -> str:
+    """What _calls.so was built for, or nothing where that is not known."""
+    if not os.path.exists(CALLS_TORCH):
+        return ""
+    with open(CALLS_TORCH, encoding="utf-8") as f:
+        return f.read()
+
+
+def _calls_stale() -> bool:
+    return _stale(CALLS, _deps(CALLS_SOURCE) | {os.path.abspath(__file__)}) or calls_torch() != installed_torch()
+
+
 def needs_build() -> bool:
-    here = {os.path.abspath(__file__)}
-    return _stale(LIB, here.union(*(_deps(s) for s in SOURCES))) or _stale(CALLS, here | _deps(CALLS_SOURCE))
+    return _stale(LIB, {os.path.abspath(__file__)}.union(*(_deps(s) for s in SOURCES))) or _calls_stale()
 
 
 def _calls_command(out):
@@ -81,9 +98,13 @@ def build(force: bool = False, verbose: bool = False) -> str:
         os.replace(o + tag, o)
     subprocess.run([NVCC, *FLAGS, "-shared", "-o", LIB + tag, *objects], check=True)
     os.replace(LIB + tag, LIB)
-    if force or _stale(CALLS, _deps(CALLS_SOURCE) | {os.path.abspath(__file__)}):
+    if force or _calls_stale():
         subprocess.run(_calls_command(CALLS + tag), check=True)
+        if os.path.exists(CALLS_TORCH):
+            os.remove(CALLS_TORCH)             # a build that stops here is of unknown origin
         os.replace(CALLS + tag, CALLS)
+        with open(CALLS_TORCH, "w", encoding="utf-8") as f:
+            f.write(installed_torch())
     return LIB
 
 
