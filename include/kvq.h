@@ -314,7 +314,8 @@ KVQ_API kvq_status kvq_compressor(const kvq_tensor* x, const kvq_tensor* w_kv, c
 /*          128 times); query head h reads key head h / (Nq / Nkv).  D        */
 /*          contiguous, token and head strides multiples of 8 elements and    */
 /*          at least D (no broadcast dimensions), data 16-byte aligned        */
-/*          (slices of one fused projection are fine).                        */
+/*          (slices of one fused projection are fine).  out may be q itself,  */
+/*          and must not overlap it otherwise, nor k and v.                    */
 /* cu_seqlens_q, cu_seqlens_k   int32 [B + 1], contiguous: sequence b holds   */
 /*          the rows [cu[b], cu[b + 1]).  cu_seqlens_k NULL: as the queries.  */
 /*          Both NULL for the 4-D form.  Rows of out that no sequence holds   */

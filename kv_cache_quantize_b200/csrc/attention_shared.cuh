@@ -1334,24 +1334,22 @@ __global__ void __launch_bounds__(SJ_THREADS, 4) shared_join_kernel(const __grid
         }
         packed[e / 2] = pack2<T>(v[0], v[1]);
     }
+    // the key offset's share of every score of the row; before the store, since out may be q
+    float off = 0.0f;
+    if (C == ATT_I8 && a.lse && a.offset_k) {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            off = __fmaf_rn(__fmul_rn(att_load<T>(a.q.base, (int64_t)b * a.q.tok + h * a.q.head + d0 + e),
+                                      __ldg(a.scale_k + kh * D + d0 + e)), __ldg(a.offset_k + kh * D + d0 + e), off);
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) off = __fadd_rn(off, __shfl_xor_sync(FULL_MASK, off, d));
+    }
     uint8_t* out = a.out.base + ((int64_t)b * a.out.tok + h * a.out.head + d0) * 2;
     if (E == 4) *reinterpret_cast<uint2*>(out) = make_uint2(packed[0], packed[E / 2 - 1]);
     else *reinterpret_cast<uint32_t*>(out) = packed[0];
-    if (a.lse) {
-        // the key offset's share of every score of the row
-        float off = 0.0f;
-        if (C == ATT_I8 && a.offset_k) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                off = __fmaf_rn(__fmul_rn(att_load<T>(a.q.base, (int64_t)b * a.q.tok + h * a.q.head + d0 + e),
-                                          __ldg(a.scale_k + kh * D + d0 + e)), __ldg(a.offset_k + kh * D + d0 + e), off);
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) off = __fadd_rn(off, __shfl_xor_sync(FULL_MASK, off, d));
-        }
-        if (lane == 0)
-            a.lse[(int64_t)b * a.Nq + h] =
-                any ? __fsub_rn(__fmul_rn(__fadd_rn(M, log2f(L)), ATT_LN2), __fmul_rn(off, a.scale)) : -INFINITY;
-    }
+    if (a.lse && lane == 0)
+        a.lse[(int64_t)b * a.Nq + h] =
+            any ? __fsub_rn(__fmul_rn(__fadd_rn(M, log2f(L)), ATT_LN2), __fmul_rn(off, a.scale)) : -INFINITY;
 }
 
 }  // namespace kvq
