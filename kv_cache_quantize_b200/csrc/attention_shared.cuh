@@ -1198,10 +1198,10 @@ __global__ void __launch_bounds__(SJ_THREADS, 4) shared_join_kernel(const __grid
     // the steps in turn) and copy.
     struct Group {
         int64_t gs, base, stats;                              // base: floats before the slots
-        int32_t k, blocks, first, count, per, copies, narrow, tile, slot, tile_rows, slot_rows, row;
+        int32_t k, blocks, first, count, per, copies, narrow, tile, slot, row;
     };
-    auto group_of = [&](int64_t gs, int k, int blocks, bool alt, int narrow, int slot, int tile, int tile_rows, int slot_rows,
-                        int row, int64_t base, int64_t stats) {
+    auto group_of = [&](int64_t gs, int k, int blocks, bool alt, int narrow, int slot, int tile, int row, int64_t base,
+                        int64_t stats) {
         Group x;
         x.gs = gs;
         x.k = k;
@@ -1213,8 +1213,6 @@ __global__ void __launch_bounds__(SJ_THREADS, 4) shared_join_kernel(const __grid
         x.narrow = narrow;
         x.tile = alt ? -1 : tile;
         x.slot = slot;
-        x.tile_rows = tile_rows;
-        x.slot_rows = slot_rows;
         x.row = row;
         x.base = base;
         x.stats = stats;
@@ -1230,10 +1228,9 @@ __global__ void __launch_bounds__(SJ_THREADS, 4) shared_join_kernel(const __grid
         if (plan.blocks > 0) gs = prefix_start(a, plan, pt, kh, &k);
         const int tile = alt ? 0 : q / TOK;
         pre = group_of(gs, k, plan.blocks, alt, alt && nreq * a.G <= 32 ? nreq * a.G : 0, pt * a.Nkv + kh, tile,
-                         plan.tile_rows, 2 * plan.tile_rows, (q - tile * TOK) * a.G + g, 0, plan.stats_area);
+                         (q - tile * TOK) * a.G + g, 0, plan.stats_area);
         mine = group_of(pre_cost + (own_before * a.Nkv + (int64_t)kh * nb) * plan.cost_own, plan.cost_own, nb, true,
-                         a.G <= 32 ? a.G : 0, b * a.Nkv + kh, 0, plan.own_rows, plan.own_slot, g, plan.own_area,
-                         plan.own_stats);
+                         a.G <= 32 ? a.G : 0, b * a.Nkv + kh, 0, g, plan.own_area, plan.own_stats);
     }
     float M = -INFINITY, L = 0.0f, acc[E];
 #pragma unroll
@@ -1256,8 +1253,6 @@ __global__ void __launch_bounds__(SJ_THREADS, 4) shared_join_kernel(const __grid
         x.narrow = own ? mine.narrow : pre.narrow;
         x.tile = own ? mine.tile : pre.tile;
         x.slot = own ? mine.slot : pre.slot;
-        x.tile_rows = own ? mine.tile_rows : pre.tile_rows;
-        x.slot_rows = own ? mine.slot_rows : pre.slot_rows;
         x.row = own ? mine.row : pre.row;
         float2 st = make_float2(-INFINITY, 0.0f);
         int64_t at = 0;
@@ -1267,7 +1262,8 @@ __global__ void __launch_bounds__(SJ_THREADS, 4) shared_join_kernel(const __grid
             const int64_t s0 = lo > 0 ? ceil_div(lo, x.k) : 0;
             const int64_t s1 = min(ceil_div(hi, x.k), (int64_t)x.blocks);
             if (s1 - s0 > (x.tile < 0 ? i : 0)) {
-                const int64_t r = (int64_t)(x.slot + c) * x.slot_rows + i * x.tile_rows + z % x.copies * x.narrow + x.row;
+                const int64_t r = (int64_t)(x.slot + c) * (own ? plan.own_slot : 2 * plan.tile_rows) +
+                                  i * (own ? plan.own_rows : plan.tile_rows) + z % x.copies * x.narrow + x.row;
                 st = reinterpret_cast<const float2*>(ws + x.stats)[r];
                 at = x.base + r * D;
             }
