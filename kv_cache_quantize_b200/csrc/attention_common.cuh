@@ -113,8 +113,7 @@ __device__ __forceinline__ int32_t own_length(const SharedArgs& a, int b) {
 template <int T>
 __device__ __forceinline__ float att_load(const uint8_t* p, int64_t i) {
     if (T == ATT_BF16) return __bfloat162float(reinterpret_cast<const __nv_bfloat16*>(p)[i]);
-    if (T == ATT_F16) return __half2float(reinterpret_cast<const __half*>(p)[i]);
-    return (float)reinterpret_cast<const int8_t*>(p)[i];
+    return __half2float(reinterpret_cast<const __half*>(p)[i]);
 }
 
 template <int T>
