@@ -9,8 +9,9 @@
  * caller owns every buffer.  Caches (and cache_scale) are updated
  * IN PLACE: only the rows addressed by a valid slot are written, and within a
  * row only the bytes the operation defines; every other byte keeps its value.
- * Execution is deterministic: each row has exactly one writer and no atomics
- * touch the outputs.
+ * Execution is deterministic: in the caches and outputs each row has exactly
+ * one writer and no atomics touch them; free_pages and fork_pages count pages
+ * and claim rows by integer atomics, whose order does not change the result.
  *
  * Tensors are passed as kvq_tensor descriptors: a DEVICE pointer to element
  * [0, ..., 0], a dtype, and shape/stride in ELEMENTS (not bytes).  The
@@ -22,7 +23,7 @@
  * failed (the status of the launch call; errors left by unrelated earlier CUDA
  * work are neither reported nor cleared), else KVQ_OK.  Data faults the
  * device can see -- a slot index outside [0, num_slots) that is not -1 --
- * skip the affected row and set a bit in a per-device fault word; a call's
+ * skip the affected row and set a bit in the device's fault word; a call's
  * KVQ_OK does not say that no such fault happened: callers that need to know
  * call kvq_get_error(), which returns and clears the bits.  Duplicate slots
  * are not detected (the pages declare the result undefined); rows then have
@@ -35,7 +36,7 @@
  *   aclnnDequantRopeQuantKvcache 算子深度解析 -- 计算步骤公式, 两段式接口与函数原型,
  *                                   约束说明, Shape 推导逻辑, Kernel 实现要点
  * The pages' two-stage GetWorkspaceSize + execute pattern becomes one call:
- * the workspace is always 0 bytes and validation happens before the launch.
+ * these operations need no workspace, and validation happens before the launch.
  */
 #ifndef KVQ_H
 #define KVQ_H
@@ -400,7 +401,10 @@ KVQ_API int64_t kvq_shared_prefix_attention_workspace(int64_t batch, int64_t n_q
 /* Pages of a cache.  Page i is element i of the first dimension of every    */
 /* cache; `caches` are up to 64 tensors [num_pages, ...] of any types (keys,  */
 /* values, scales, several layers), each page contiguous and at most 2^31-1   */
-/* bytes, only the page dimension strided.  They must not overlap.            */
+/* bytes, only the page dimension strided.  They must not overlap.  Copies go */
+/* by 16 bytes where all caches' addresses, strides and page sizes allow it,  */
+/* else by 4, else by single bytes, so one side tensor of odd pages slows all  */
+/* (4001 pages of 2 x 32 KB: 85 us; beside pages of 260 bytes 150, of 257 450). */
 /* ref_count   int32 [num_pages], contiguous: the table rows that hold a      */
 /*             page; 0: free.                                                  */
 /* block_table int32 [rows, cols], columns contiguous: a row's pages in token */
@@ -417,9 +421,11 @@ KVQ_API kvq_status kvq_copy_pages(const kvq_tensor* caches, int32_t n_caches, co
                                   const kvq_tensor* dst, kvq_stream stream);
 
 /* free_pages: each named row gives up its pages (ref_count - 1), its entries
- * become -1 and its length 0.  Empty rows, rows named twice and -1 are no-ops
- * the second time; rows, pages or lengths out of range, and pages that are
- * free already, are skipped and set KVQ_FAULT_SLOT_RANGE. */
+ * become -1 and its length 0.  Empty rows, -1, and a row named again are
+ * no-ops.  Rows out of range, and entries that are out of range or whose page
+ * is free already, are skipped and set KVQ_FAULT_SLOT_RANGE.  So does a length
+ * out of range, but its row is emptied all the same: a negative one gives up
+ * no page, one that the row cannot hold all the row's entries. */
 KVQ_API kvq_status kvq_free_pages(kvq_tensor* block_table, kvq_tensor* seq_lens, kvq_tensor* ref_count,
                                   const kvq_tensor* rows, int64_t block_size, kvq_stream stream);
 
@@ -441,7 +447,9 @@ KVQ_API kvq_status kvq_fork_pages(const kvq_tensor* caches, int32_t n_caches, kv
  * U stay, the others take the free ones below U, both in ascending order.
  * page_map (int32 [num_pages]) receives each page's new number (-1: free);
  * new_table and new_ref_count the renumbered table and counts (either may be
- * the old one; else the old one is left as it is).  Two kernels on `stream`. */
+ * the old one; else the old one is left as it is).  An entry whose page is
+ * free becomes -1; one out of range too, and sets KVQ_FAULT_SLOT_RANGE.  Two
+ * kernels on `stream`. */
 KVQ_API kvq_status kvq_compact_pages(const kvq_tensor* caches, int32_t n_caches, const kvq_tensor* block_table,
                                      const kvq_tensor* ref_count, kvq_tensor* new_table, kvq_tensor* new_ref_count,
                                      kvq_tensor* page_map, kvq_stream stream);
@@ -451,10 +459,10 @@ KVQ_API kvq_status kvq_compact_pages(const kvq_tensor* caches, int32_t n_caches,
 /* ------------------------------------------------------------------------ */
 
 /* Read and clear the current device's fault word: enqueues on `stream` one
- * kernel that atomically exchanges the word with 0 (after every earlier
- * kernel of the stream has completed), copies that value back, waits for
- * `stream` and stores the bits in *fault_bits.  Because the read and the
- * clear are one atomic operation, a bit raised by a kernel on another stream
+ * kernel that atomically exchanges it with 0 (a word for each of the library's
+ * three units; after every earlier kernel of the stream has completed), copies
+ * the bits back, waits for `stream` and stores them in *fault_bits.  Because
+ * the read and the clear of a word are one atomic operation, a bit raised by a kernel on another stream
  * is returned either by this call or by the next one, never lost.  Returns
  * KVQ_ERR_CUDA if the launch, the copy or the stream reported an error (the
  * bits are then 0). */

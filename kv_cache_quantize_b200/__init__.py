@@ -390,7 +390,7 @@ def prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqle
     """Causal attention over whole prompts with grouped heads (see kvq_prompt_attention): q [T, Nq, D] with
     cu_seqlens_q [B + 1] (packed sequences of different lengths), or q [B, S, Nq, D]; k and v with Nkv heads,
     cu_seqlens_k where a sequence has other keys than queries (a cached context in front).  Returns out, like q;
-    rows that no sequence holds are not written.  softmax_scale defaults to D ** -0.5.  Spans outside the tensors
+    rows that no sequence holds are not written.  Forward only: out has no autograd history.  softmax_scale defaults to D ** -0.5.  Spans outside the tensors
     are reported by get_error(), or raised here with check=True."""
     call = _calls().prompt_attention
     if stream is None:
@@ -419,7 +419,7 @@ def shared_prefix_attention(q: torch.Tensor, k_cache: torch.Tensor, v_cache: tor
     """Attention of one new token per request over a paged cache (see kvq_shared_prefix_attention): the first
     prefix_len keys, in the pages of prefix_table, are shared by all requests and read once; request b's own
     seq_lens[b] keys follow in the pages block_table[b].  int8 caches need scale_k and scale_v.  Returns out, like
-    q [B, Nq, D]; rows with seq_lens -1 are not written.  The workspace is allocated when not given (uint8,
+    q [B, Nq, D]; rows with seq_lens -1 are not written.  Forward only: out has no autograd history.  The workspace is allocated when not given (uint8,
     shared_prefix_attention_workspace() bytes, one per call that may run at the same time).  Bad pages and lengths
     are reported by get_error(), or raised here with check=True."""
     call = _calls().shared_prefix_attention
@@ -483,7 +483,7 @@ def compact_pages(caches: Sequence[torch.Tensor], block_table: torch.Tensor, ref
 # ---------------------------------------------------------------------------
 def get_error(stream=None, device=None) -> int:
     """Wait for the stream, return and clear the fault bits (FAULT_SLOT_RANGE, FAULT_TIMEOUT, FAULT_NO_PAGE) of the
-    device in one atomic read-and-clear on the device.  The device is `device`, else the
+    device, one atomic read-and-clear on the device for each of the library's three units.  The device is `device`, else the
     stream's, else the current one."""
     if device is None and isinstance(stream, torch.cuda.Stream):
         device = stream.device

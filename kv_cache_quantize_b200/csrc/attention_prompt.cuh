@@ -19,9 +19,11 @@
 //                   block j + 1, tile 0 and tile 1 in turn;
 //   warp 9          work items and TMA: the grid has a CTA for every item, but a
 //                   running CTA takes over items whose CTAs have not started
-//                   (cluster launch control), heavy ones first (against a
-//                   fixed assignment 243 -> 215 us for 24 prompts of 1 to
-//                   2048 tokens); Q tiles, and a ring of K and V tiles of 128
+//                   (cluster launch control; against a fixed assignment 243 ->
+//                   215 us for 24 prompts of 1 to 2048 tokens): sequences in
+//                   the order given, the heavy items of each first (longest
+//                   sequence last instead of first: 197 instead of 194 us);
+//                   Q tiles, and a ring of K and V tiles of 128
 //                   keys (128-byte swizzle; 5 stages, 4 cost 4 %).
 // The tensor pipe executes a CTA's products in order, so Q K^T of block j + 1
 // may overwrite the columns that P V of block j reads.
@@ -33,7 +35,9 @@
 // 128, bf16: 862 us, 1278 TFLOP/s, 0.78 of the measured peak on a cold card;
 // 0.68 in a loop, where the power cap lowers the clock.  An item's start and end
 // cost about three blocks, so short prompts are slower: 24 of 1 to 2048 tokens
-// 205 us, 660 TFLOP/s.
+// 205 us, 660 TFLOP/s.  At D = 64 the products halve and the softmax does not:
+// 16384 tokens 768 us, 716 TFLOP/s.  Keys are not split: few queries behind
+// many keys fill few SMs (16 tokens behind 100000: 4 items, 1370 us).
 //
 // A row's weights are rounded to the 16-bit type of V for the product (half a
 // step, the rounding that the output itself gets); their sum is taken before.

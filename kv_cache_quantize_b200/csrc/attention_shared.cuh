@@ -45,11 +45,12 @@
 // What bounds it (one B200; times of both kernels): over a long prefix the
 // chain of a tile's softmax and products, as in the prompt kernel, with the
 // scores read twice from TMEM for want of registers -- 256 requests over 32768
-// bf16 keys 87 us (0.49 of the measured peak), over int8 ones 101 us; over own
-// keys, int8, shared memory: 224 KB pass through it for a step of 128 keys (raw
-// codes in and out, f16 tiles in, operands of the products), 1750 cycles --
-// 256 requests of 512 own keys 62 us, 134 MB (2.2 TB/s); bf16 63 us, 268 MB
-// (4.3 TB/s).  One step of one request takes 10 us, two launches among it.
+// bf16 keys 90 us (0.46 of the measured peak), over int8 ones 105 us, with f16
+// queries 116; over own keys, int8, shared memory: 224 KB pass through it for a
+// step of 128 keys (raw codes in and out, f16 tiles in, operands of the
+// products), 1750 cycles -- 256 requests of 512 own keys 64 us, 134 MB (2.1
+// TB/s; 69 us from a cold L2), f16 queries 72; bf16 66 us, 268 MB (4.0 TB/s;
+// cold 79).  One step of one request takes 12 us, two launches among it.
 //
 // Pages of 8, 16, 32 .. tokens come by TMA, a box of up to 128 tokens of one
 // page.  Other page sizes come
@@ -92,7 +93,9 @@ __host__ __device__ constexpr uint32_t sa_smem_bytes(int D, bool i8) {
 // (prefix), a request's own keys over int8 and over 16-bit pages.  Measured
 // with own steps at 3 (as two tiles) and at 2: 40 requests, prefix 2000, own 1
 // to 1500, bf16: 41 and 32 us; 256 requests, prefix 32768, own 1 to 1024, int8:
-// 235 and 220 us.
+// 235 and 220 us.  A piece's own start and end are not in it: the CTAs that get
+// the pieces of 256 lists of one step have 48 of them each and end last (prefix
+// 32768 bf16: 90 us without own keys, 168 with 16 of each request).
 constexpr int SA_COST2 = 3, SA_COST1 = 2, SA_COST_OWN8 = 2, SA_COST_OWN16 = 2;
 
 struct SharedPlan {
@@ -686,7 +689,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
                 const uint32_t slot = n_item % SA_ITEMS;
                 if (!__all_sync(FULL_MASK, mbar_wait_ns(&item_full[slot], (n_item / SA_ITEMS) & 1u, SA_WAIT_NS))) break;
                 const int n = items[slot].steps, own = items[slot].own, b0 = items[slot].b0, kh = items[slot].kh;
-            const bool alt = items[slot].alt != 0;
+                const bool alt = items[slot].alt != 0;
                 const int key0 = items[slot].key0, keys = items[slot].keys;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&item_empty[slot]);
@@ -694,9 +697,8 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             }
             drain_tiles(tile_no);
         }
-        // ---------------- Q times the key scale ----------------
         if (blockIdx.x == 0 && warp == 14) {
-            // for the join: the own steps of the requests before each one
+            // ---------------- for the join: the own steps of the requests before each one ----------------
             int32_t* before = reinterpret_cast<int32_t*>(reinterpret_cast<float*>(a.workspace) + plan.before);
             int32_t sum = 0;
             for (int b0 = 0; b0 < a.B; b0 += 32) {
@@ -713,6 +715,7 @@ __global__ void __launch_bounds__(SA_THREADS, 1)
             if (lane == 0) before[a.B] = sum;
         }
         if (I8 && warp == 14) {
+            // ---------------- Q times the key scale ----------------
             uint32_t used[2] = {0, 0};
             int q_next = 0;
             bool ok = true;

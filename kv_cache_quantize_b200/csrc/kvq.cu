@@ -14,8 +14,8 @@
 namespace {
 
 // ---------------------------------------------------------------------------
-// fault word read-and-clear (kvq_get_error): one atomic exchange on the device
-// into a snapshot slot that the host then copies back
+// fault word read-and-clear (kvq_get_error): an atomic exchange of each unit's
+// word on the device, joined in a snapshot slot that the host then copies back
 // ---------------------------------------------------------------------------
 constexpr uint32_t FAULT_SNAPSHOTS = 64;
 __device__ unsigned int g_fault_snapshot[FAULT_SNAPSHOTS];
@@ -1007,7 +1007,7 @@ kvq_status kvq_get_error(kvq_stream stream, uint32_t* fault_bits) {
     if (!fault_bits) return KVQ_ERR_NULL;
     *fault_bits = 0u;
     cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-    // one device-side atomic exchange reads and clears the word, so a bit
+    // a device-side atomic exchange reads and clears each unit's word, so a bit
     // raised by a kernel on another stream is either returned by this call or
     // left for the next one; concurrent callers take different snapshot slots
     static std::atomic<uint32_t> ticket{0};
